@@ -357,6 +357,193 @@ int sgemv_list_table(const sgemv_task* tasks, int32_t count, int32_t B, void* ta
  * EHIP. */
 int sgemv_run_list_table(const void* table_dev, const sgemv_list_launch* launch, void* hip_stream);
 
+/* ------------------------------------------------------------------------
+ * The operators between the GEMVs of a decode step. The products q, k and v
+ * of a layer go on to rotary positions and the cache, the attention's output
+ * to the o projection, the vocabulary product's to the choice of a token
+ * (P1 §1 runs these per token, and verifies all candidates of a prefix tree
+ * in one step; the page describes none of them, the definitions below are
+ * this library's). All lengths, page tables and positions are read on the
+ * device, so a captured launch can be replayed while they change.
+ * ------------------------------------------------------------------------ */
+
+enum { SGEMV_F16 = 0, SGEMV_BF16 = 1, SGEMV_F32 = 2 };   /* element types */
+
+/* Rows of tokens x heads x head_dim values in device memory, 16-byte
+ * aligned. Strides count elements and are multiples of 8 (the stride of
+ * something there is only one of is not used); columns are contiguous.
+ * head_dim: a multiple of 8 up to 256. dtype: SGEMV_F16 or SGEMV_BF16. */
+typedef struct sgemv_rows {
+  void* data;
+  int64_t token_stride, head_stride;
+  int32_t tokens, heads, head_dim, dtype;
+} sgemv_rows;
+
+/* A paged cache of keys and values: element (page, slot, head, column) of K
+ * at k[page * k_page + slot * k_slot + head * k_head + column], and of V
+ * likewise. Alignment and strides as sgemv_rows. page_size: a power of two,
+ * 8..65536 slots. */
+typedef struct sgemv_cache {
+  void *k, *v;
+  int64_t k_page, k_slot, k_head;
+  int64_t v_page, v_slot, v_head;
+  int32_t pages, page_size, heads, head_dim, dtype;
+} sgemv_cache;
+
+/* Sequences and their new tokens, in device memory. Sequence s has the new
+ * tokens new_start[s] .. new_start[s + 1] - 1 of the rows passed beside it
+ * (none is fine) and ctx_len[s] tokens in all, new ones included; new token i
+ * of n has slot ctx_len[s] - n + i, and slot p lies in page
+ * pages[s * pages_stride + p / page_size]. new_start does not decrease. Rows
+ * before new_start[0] and from new_start[count] on belong to nobody and stay
+ * as they are. Nothing is read or written out of range whatever these arrays
+ * hold: ctx_len counts up to pages_per_seq pages (and 2^30 slots), a token
+ * of a slot below 0 is not stored and sees no key, and a page index outside
+ * [0, pages) is a page that is not there: nothing is stored in it, and its
+ * keys are not visible. */
+typedef struct sgemv_seqs {
+  const int32_t* new_start;  /* [count + 1]              */
+  const int32_t* ctx_len;    /* [count]                  */
+  const int32_t* pages;      /* [count][pages_per_seq]   */
+  int64_t pages_stride;      /* elements                 */
+  int32_t count, pages_per_seq;
+} sgemv_seqs;
+
+/* Rotary positions. Pair j of a head's first rot_dim columns, (j, j + rot/2)
+ * or, interleaved, (2j, 2j + 1), turns by turns[j] * position whole turns:
+ * (a, b) <- magnitude * (a cos - b sin, a sin + b cos). Columns from rot_dim
+ * on stay as they are. */
+typedef struct sgemv_rope_t {
+  const double* turns;       /* device [rot_dim / 2], from sgemv_rope_table */
+  int32_t rot_dim;           /* even, 2..head_dim                           */
+  int32_t interleaved;       /* 0 or 1                                      */
+  float magnitude;           /* > 0, finite; 1 for plain rotary positions   */
+} sgemv_rope_t;
+
+/* sgemv_rope_table - turns per position of each pair: f_j =
+ * base^(-2j/rot_dim) / (2 pi), stretched for contexts longer than trained:
+ * context = 0 divides every f_j by `factor`; context > 0 blends by the turns
+ * r = context f_j that a pair makes over the trained context: with
+ * g = clamp((r - low) / (high - low), 0, 1), f_j (g + (1 - g) / factor), so
+ * fast pairs stay and slow ones are divided.
+ *   turns_out : host double[rot_dim / 2].
+ * Errors: EINVAL (rot_dim odd or outside 2..256; base <= 0, factor <= 0,
+ * context < 0, high <= low with a context, anything not finite; NULL). */
+int sgemv_rope_table(int32_t rot_dim, double base, double factor, double context, double low, double high,
+                     double* turns_out);
+
+/* sgemv_rope - rotary positions alone: out = x turned, at positions[token]
+ * (device int32[tokens], any value). out may be x itself; otherwise they do
+ * not overlap. Angles in 64 bits, products in FP32, one rounding.
+ * Enqueues one kernel and returns without synchronising.
+ * Errors: EINVAL, EALIGN, ESIZE (2^24 tokens or more), EHIP. */
+int sgemv_rope(const sgemv_rope_t* rope, const int32_t* positions_dev, const sgemv_rows* x, const sgemv_rows* out,
+               void* hip_stream);
+
+/* sgemv_append - the new tokens' rotary positions and their append to the
+ * cache, in one kernel: q_out = q turned, K[slot] = k turned, V[slot] = v.
+ *   rope          : NULL to store k as it is (q and q_out are NULL then).
+ *   positions_dev : device int32[tokens], or NULL for each token's slot
+ *                   (candidates of one depth share a position, not a slot).
+ *   q, q_out      : both or neither; q_out may be q itself.
+ *   k, v          : tokens x cache->heads, the cache's type.
+ * No two new tokens may have the same slot. Apart from q_out = q nothing
+ * overlaps. Numerics as sgemv_rope; v is copied bit for bit.
+ * Errors: EINVAL, EALIGN, ESIZE (2^24 tokens or more), EHIP. */
+int sgemv_append(const sgemv_cache* cache, const sgemv_seqs* seqs, const sgemv_rope_t* rope, const int32_t* positions_dev,
+                 const sgemv_rows* q, const sgemv_rows* q_out, const sgemv_rows* k, const sgemv_rows* v, void* hip_stream);
+
+/* What sgemv_attend enqueues (filled by sgemv_attend_plan). */
+typedef struct sgemv_attend_plan_t {
+  int64_t workspace_bytes;  /* device scratch of one call; 0: none                       */
+  int64_t grid;             /* workgroups of the first kernel                            */
+  int64_t lds_bytes;        /* dynamic LDS per workgroup                                 */
+  int32_t block;            /* lanes per workgroup                                       */
+  int32_t tile_rows;        /* (token, query head) rows of a workgroup                   */
+  int32_t block_keys;       /* keys of a step                                            */
+  int32_t splits;           /* parts of the context; over 1, a second kernel joins them  */
+} sgemv_attend_plan_t;
+
+/* sgemv_attend_plan - the launch sgemv_attend would make for `tokens` rows of
+ * `heads` query heads, without any HIP call. cache and seqs as they will be
+ * passed (device pointers are checked, not read).
+ *   max_ctx : the longest sequence the caller expects, or 0 for what
+ *             pages_per_seq pages hold. It shapes the launch only: longer
+ *             sequences are computed just as well.
+ * Errors: EINVAL, EALIGN, ESIZE. */
+int sgemv_attend_plan(const sgemv_cache* cache, const sgemv_seqs* seqs, int32_t tokens, int32_t heads, int32_t max_ctx,
+                      sgemv_attend_plan_t* out);
+
+/* sgemv_attend - softmax attention of the new tokens over the cache, which
+ * holds them already: for new token i and query head h,
+ * out = sum_t p_t V[t] / sum_t p_t with p_t = exp(scale q . K[t]) over the
+ * visible slots t, of cache head h / (q->heads / cache->heads).
+ *   q, out     : tokens x heads, heads a multiple of cache->heads; the
+ *                cache's type and head_dim.
+ *   scale      : > 0, at most 1e30; 1/sqrt(head_dim) as a rule.
+ *   tree_dev   : NULL: a token sees the slots up to its own. Otherwise
+ *                uint32[tokens][tree_words]: it sees every slot before its
+ *                sequence's new tokens, and new token j of its sequence where
+ *                bit j % 32 of word j / 32 of its row is set (candidates that
+ *                share a prefix, verified in one step). Bits past tree_words
+ *                count as 0.
+ *   workspace_dev : scratch of at least workspace_bytes as sgemv_attend_plan
+ *                says, 16-byte aligned (NULL where that is 0); not shared by
+ *                calls that may run at the same time. What it holds before
+ *                does not matter.
+ * A token that sees nothing gets zeros. A slot that a token does not see has
+ * no part in its result, whatever it holds (infinities and NaN included), and
+ * so have slots behind a sequence's end.
+ * Numerics: scores, the running maximum, sums and outputs in FP32; each p_t
+ * relative to the row's maximum rounded to the cache's type; one rounding at
+ * the end: |out - exact| <= about (3 u + e) max_t |V[t]| with u the type's
+ * half step and e FP32's over the scores' size. Deterministic for one plan.
+ * Enqueues one kernel, or two with splits, and returns without synchronising.
+ * out overlaps nothing else. Errors: EINVAL, EALIGN, ESIZE (sizes beyond the
+ * grid, workspace too small), EHIP. */
+int sgemv_attend(const sgemv_cache* cache, const sgemv_seqs* seqs, const sgemv_rows* q, const sgemv_rows* out, float scale,
+                 const uint32_t* tree_dev, int32_t tree_words, int32_t max_ctx, void* workspace_dev, int64_t workspace_bytes,
+                 void* hip_stream);
+
+/* Penalties, biases and masks on rows of logits; all pointers are device
+ * memory. x and out: `rows` rows of `vocab` values, element aligned, strides
+ * in elements. out_dtype: dtype, or SGEMV_F32. out may be x (same type and
+ * stride); otherwise nothing overlaps. */
+typedef struct sgemv_logits {
+  const void* x;
+  void* out;
+  int64_t x_stride, out_stride;
+  const int32_t* hist_start;   /* [rows + 1] each row's part of hist_ids; NULL: no histories       */
+  const int32_t* hist_ids;     /* [n_hist] token ids; those outside 0..vocab-1 count for nothing   */
+  int64_t n_hist;
+  const int32_t* prompt_len;   /* [rows] how many of a row's ids are its prompt's; NULL: none      */
+  const float* repetition;     /* [rows] each; NULL: 1                                             */
+  const float* frequency;      /*        NULL: 0                                                   */
+  const float* presence;       /*        NULL: 0                                                   */
+  const int32_t* bias_start;   /* [rows + 1] each row's part of the bias list; NULL: no biases     */
+  const int32_t* bias_ids;     /* [n_bias] token ids, as hist_ids                                  */
+  const float* bias_values;    /* [n_bias]                                                         */
+  int64_t n_bias;
+  const uint32_t* masks;       /* [n_masks] masks of (vocab + 31) / 32 words: bit v % 32 of word   */
+  int64_t mask_stride;         /* v / 32 set: token v is allowed; stride in words                  */
+  const int32_t* mask_row;     /* [rows] mask of each row, none where outside 0..n_masks-1; NULL:  */
+                               /* mask i for row i (n_masks = rows then)                           */
+  int32_t n_masks;             /* 0 with masks NULL                                                */
+  int32_t rows, vocab;
+  int32_t dtype, out_dtype;
+} sgemv_logits;
+
+/* sgemv_adjust_logits - in this order, in FP32, rounded once:
+ *   l <- l > 0 ? l / repetition : l * repetition  for ids in the history
+ *   l <- l - frequency n - presence               for ids n > 0 times behind the prompt
+ *   l <- l + bias                                 (an id given twice: its last place holds)
+ *   l <- -inf                                     for ids the row's mask does not allow
+ * A grammar or a prefix tree gives its states' allowed tokens as masks. A row
+ * may be left with none: all -inf. Enqueues one kernel and returns without
+ * synchronising; the same bits on every call.
+ * Errors: EINVAL, EALIGN, ESIZE (over 65535 rows), EHIP. */
+int sgemv_adjust_logits(const sgemv_logits* g, void* hip_stream);
+
 /* sgemv_strerror - static description of a status code (never NULL). */
 const char* sgemv_strerror(int code);
 

@@ -11,3 +11,6 @@ from .sgemv import (  # noqa: F401
     describe_fp16, pack_fp16, layout_fp16, f64_to_f16, probe_read, probe_empty,
     LIST_MAX, run_list, plan_list, LIST_TABLE_MAX, ListLaunch, list_table, run_list_table,
 )
+from .decode import (  # noqa: F401
+    Rope, Sequences, PagedCache, adjust_logits, rope_table, AttendPlan,
+)

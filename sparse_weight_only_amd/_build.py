@@ -14,9 +14,10 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libsgemv.so")
-HOST_SRCS = ["host_pack.cpp", "host_layout.cpp"]
+HOST_SRCS = ["host_pack.cpp", "host_layout.cpp", "host_rope.cpp"]
 HIP_SRCS = ["sgemv_k_nk1.hip", "sgemv_k_nk2.hip", "sgemv_k_nk4.hip", "sgemv_k_f16.hip", "sgemv_k_rb.hip", "sgemv_launch.hip",
-            "sgemv_probe.hip", "sgemv_k_list.hip"]
+            "sgemv_probe.hip", "sgemv_k_list.hip",
+            "decode_rope.hip", "attend_k_few.hip", "attend_k_many.hip", "attend_launch.hip", "decode_logits.hip"]
 
 
 def _hipcc() -> str:

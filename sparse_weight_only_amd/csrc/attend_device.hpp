@@ -1,0 +1,181 @@
+// Attention of new tokens over a paged cache: device code.
+//
+// Row (token i, query head hq) of a sequence with keys k_t and values v_t:
+//   o = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale q . k_t - m),
+// over the visible keys t, in one pass: m is the running maximum of the
+// scores, and what was summed under an older maximum is scaled down when it
+// grows. Scores, m, the sum of the p_t and the output are kept in FP32; p_t is
+// rounded to the cache's type for the second product (half a step of at most
+// 1, the same step as the result's own rounding), its sum is not.
+//
+// Both products run on the matrix cores, the first transposed (keys x rows),
+// so that a lane holds scores of one row only: the row statistics are a
+// reduction over the lane's own registers and one or two lane swaps, and the
+// scores become the second product's operand without leaving the lane. That
+// operand wants 8 keys in a row from each lane; the lane has runs of 4, so the
+// keys of a step are numbered by where they are, and V is read in that order.
+#pragma once
+#include "decode_device.hpp"
+
+namespace sgemv_dev {
+
+struct AttendParams {
+  SeqView seq;
+  const uint16_t *k, *v, *q;
+  uint16_t* out;
+  int64_t k_page, k_slot, k_head, v_page, v_slot, v_head;
+  int64_t q_token, q_head, o_token, o_head;
+  const uint32_t* tree;   // [tokens][tree_words], or null: a token sees the slots up to its own
+  int32_t tree_words;
+  int32_t group;          // query heads per cache head
+  int32_t heads;          // cache heads
+  int32_t dim;
+  int32_t splits;         // parts of the context, joined by attend_join_kernel
+  int32_t slots;          // row tiles, empty ones included
+  float scale2;           // scale * log2(e): scores in powers of two
+  float* part;            // splits > 1: [row][split][dim] sums, then [row][split] of (m, sum of p)
+};
+typedef void (*AttendFn)(AttendParams);
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 b16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 b16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t dword2 __attribute__((ext_vector_type(2)));
+
+template <class T> struct Half;
+template <> struct Half<_Float16> {
+  static __device__ __forceinline__ f32x4 mma16(dword4 a, dword4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x16 mma32(dword4 a, dword4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ uint32_t pack(float a, float b) { return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b}); }
+  static __device__ __forceinline__ float lo(uint32_t u) { return (float)__builtin_bit_cast(f16x2, u).x; }
+  static __device__ __forceinline__ float hi(uint32_t u) { return (float)__builtin_bit_cast(f16x2, u).y; }
+};
+template <> struct Half<__bf16> {
+  static __device__ __forceinline__ f32x4 mma16(dword4 a, dword4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b16x8, a), __builtin_bit_cast(b16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x16 mma32(dword4 a, dword4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b16x8, a), __builtin_bit_cast(b16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ uint32_t pack(float a, float b) { return __builtin_bit_cast(uint32_t, b16x2{(__bf16)a, (__bf16)b}); }
+  static __device__ __forceinline__ float lo(uint32_t u) { return __builtin_bit_cast(float, u << 16); }
+  static __device__ __forceinline__ float hi(uint32_t u) { return __builtin_bit_cast(float, u & 0xffff0000u); }
+};
+
+// What lanes read in the place of a key that is not there: V's rows have to
+// be zeros even where their weight is 0 (0 * NaN), K's may be anything.
+static __device__ const dword4 kNothing[2] = {};
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+// max and sum with the lane 16 or 32 places away
+struct Two { float a, b; };
+__device__ __forceinline__ Two both_x32(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const uint32_t a = r[0], b = r[1];
+  return Two{__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)};
+}
+__device__ __forceinline__ Two both_x16(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const uint32_t a = r[0], b = r[1];
+  return Two{__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)};
+}
+__device__ __forceinline__ float max_x32(float x) { const Two t = both_x32(x); return fmaxf(t.a, t.b); }
+__device__ __forceinline__ float max_x16(float x) { const Two t = both_x16(x); return fmaxf(t.a, t.b); }
+__device__ __forceinline__ float sum_x32(float x) { const Two t = both_x32(x); return t.a + t.b; }
+__device__ __forceinline__ float sum_x16(float x) { const Two t = both_x16(x); return t.a + t.b; }
+
+// The rows of a tile are (new token, query head of the group) pairs of one
+// sequence and cache head: row r is token r / group, head r % group, so a
+// tile of a shared head reads its keys once for the whole group.
+//
+// Tiles of M rows are numbered without a pass over the sequences: sequence s
+// has the slots from floor(start(s) group / M) + s on, at least as many as its
+// tiles, since floor(a + b) - floor(a) + 1 >= ceil(b); what is left over is
+// empty. floor(tokens group / M) + count slots in all.
+struct Tile {
+  int s, first, n;          // sequence, its first new token, its new tokens
+  int old;                  // slot of its first new token
+  int row0, rows;           // first row of the tile, rows of the sequence
+  int end, full;            // keys any row sees, keys every row sees
+  int key0, key1;           // this split's part of [0, end)
+  const int32_t* pages;
+};
+
+__device__ __forceinline__ int64_t slot_base(const AttendParams& p, int s, int m) {
+  return (int64_t)p.seq.start(s) * p.group / m + s;
+}
+
+// The keys of the tile at `row0` of sequence t.s, and split `split` of them in
+// whole blocks of `block` keys.
+__device__ __forceinline__ void tile_keys(const AttendParams& p, int m, int block, int split, Tile& t) {
+  const int ctx = p.seq.ctx(t.s);
+  t.old = ctx - t.n;
+  if (p.tree) {
+    t.end = ctx;
+    t.full = t.old;
+  } else {
+    const int last = t.row0 + m < t.rows ? (t.row0 + m - 1) / p.group : t.n - 1;
+    t.end = t.old + last + 1;
+    t.full = t.old + t.row0 / p.group + 1;
+  }
+  t.end = t.end < 0 ? 0 : t.end > ctx ? ctx : t.end;
+  const int blocks = (t.end + block - 1) / block;
+  const int per = (blocks + p.splits - 1) / p.splits * block;
+  const int64_t k0 = (int64_t)split * per;
+  t.key0 = k0 < t.end ? (int)k0 : t.end;
+  t.key1 = k0 + per < t.end ? (int)(k0 + per) : t.end;
+}
+
+__device__ __forceinline__ bool find_tile(const AttendParams& p, int m, int block, int slot, int split, Tile& t) {
+  t.s = wave_upper(p.seq.count, slot, [&](int i) { return slot_base(p, i, m); });
+  t.first = p.seq.start(t.s);
+  t.n = p.seq.start(t.s + 1) - t.first;
+  t.rows = t.n * p.group;
+  const int64_t at = slot - slot_base(p, t.s, m);
+  if (t.n <= 0 || at < 0 || at * m >= t.rows) return false;
+  t.row0 = (int)at * m;
+  t.pages = p.seq.pages + t.s * p.seq.pages_stride;
+  tile_keys(p, m, block, split, t);
+  return true;
+}
+
+// Bit b: whether new token `i` of the tile's sequence sees key kb + b.
+__device__ __forceinline__ uint32_t seen_bits(const AttendParams& p, const Tile& t, int i, int kb) {
+  int n;
+  uint32_t bits = ~0u;
+  if (p.tree) {
+    // the words of this row, from new token kb - old on; older keys are seen
+    const int at = kb - t.old;
+    const uint32_t* w = p.tree + (int64_t)(t.first + i) * p.tree_words;
+    const int w0 = at >> 5, sh = at & 31;      // rounds down for at < 0 too
+    const uint32_t a = w0 < 0 ? ~0u : w0 < p.tree_words ? w[w0] : 0u;
+    const uint32_t b = w0 + 1 < 0 ? ~0u : w0 + 1 < p.tree_words ? w[w0 + 1] : 0u;
+    bits = sh ? (a >> sh) | (b << (32 - sh)) : a;
+    n = t.end - kb;
+  } else {
+    n = t.old + i + 1 - kb;
+    n = n < t.end - kb ? n : t.end - kb;
+  }
+  return n >= 32 ? bits : n <= 0 ? 0u : bits & ((1u << n) - 1u);
+}
+
+__device__ __forceinline__ bool not_finite(float x) { return !(__builtin_fabsf(x) < __builtin_inff()); }
+
+// Where a row's part of the sums goes when the context is split.
+__device__ __forceinline__ float* part_sums(const AttendParams& p, int64_t row, int split) {
+  return p.part + (row * p.splits + split) * p.dim;
+}
+__device__ __forceinline__ float* part_stats(const AttendParams& p, int64_t row, int split) {
+  return p.part + (int64_t)p.seq.tokens * p.heads * p.group * p.splits * p.dim + (row * p.splits + split) * 2;
+}
+
+}  // namespace sgemv_dev

@@ -8,6 +8,7 @@
 
 #include "internal.hpp"
 #include "kernels.hpp"
+#include "launch_util.hpp"
 #include "sgemv_device.hpp"
 #include "sgemv_list_device.hpp"
 
@@ -19,6 +20,29 @@ static_assert(sgemv_dev::kMaxGroup == SGEMV_MAX_GROUP, "group size limit");
 static_assert(sgemv_dev::kListMax == SGEMV_LIST_MAX, "list size limit");
 using sgemv_dev::KernelFn;
 using sgemv_dev::KParams;
+
+namespace sgemv {
+
+// Dynamic LDS beyond 64 KiB needs the kernel's limit raised. The runtime
+// keeps the attribute per kernel and device, so it is set once for each
+// (kernel, device) pair, to the full 160 KiB, and remembered here.
+int ensure_lds(const void* fn, int64_t lds_bytes) try {
+  if (lds_bytes <= 65536) return SGEMV_OK;
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return SGEMV_EHIP;
+  static std::mutex mu;
+  static std::vector<std::pair<const void*, int>> raised;
+  std::lock_guard<std::mutex> lock(mu);
+  for (const auto& e : raised)
+    if (e.first == fn && e.second == dev) return SGEMV_OK;
+  if (hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024) != hipSuccess) return SGEMV_EHIP;
+  raised.emplace_back(fn, dev);
+  return SGEMV_OK;
+} catch (...) {   // the record could not grow: nothing may leave a C entry point
+  return SGEMV_EHIP;
+}
+
+}  // namespace sgemv
 
 namespace {
 
@@ -97,23 +121,6 @@ KParams make_params(const sgemv_desc* d, const void* blob, const void* x, void* 
   for (int c = 0; c < 4; ++c) p.cls_row[c + 1] = p.cls_row[c] + d->class_rows[c];
   p.waves = L.waves;
   return p;
-}
-
-// Dynamic LDS beyond 64 KiB needs the kernel's limit raised. The runtime
-// keeps the attribute per kernel and device, so it is set once for each
-// (kernel, device) pair, to the full 160 KiB, and remembered here.
-int ensure_lds(const void* fn, int64_t lds_bytes) {
-  if (lds_bytes <= 65536) return SGEMV_OK;
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return SGEMV_EHIP;
-  static std::mutex mu;
-  static std::vector<std::pair<const void*, int>> raised;
-  std::lock_guard<std::mutex> lock(mu);
-  for (const auto& e : raised)
-    if (e.first == fn && e.second == dev) return SGEMV_OK;
-  if (hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024) != hipSuccess) return SGEMV_EHIP;
-  raised.emplace_back(fn, dev);
-  return SGEMV_OK;
 }
 
 bool aligned(const void* blob, const void* x, const void* y) {

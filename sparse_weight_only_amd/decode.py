@@ -1,0 +1,368 @@
+"""The operators between the GEMVs of a decode step, on torch tensors.
+
+``PagedCache.append`` (rotary positions and the append to a paged cache),
+``PagedCache.attend`` (attention of the new tokens over it), ``Rope.apply``
+(rotary positions alone) and ``adjust_logits`` (penalties, biases and grammar
+masks) check their tensors, marshal them into the C ABI's structures
+(``include/sgemv.h``) and enqueue on the current stream or on ``stream``.
+Everything is computed by the library; lengths, page tables and positions are
+read on the device when the kernels run, so a captured call can be replayed
+while they change. Tensors that a call makes (outputs, scratch) belong to the
+stream that it runs on.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import numpy as np
+
+from .sgemv import SgemvError, _check, _ptr, lib, SGEMV_EALIGN, SGEMV_EINVAL, SGEMV_ESIZE  # noqa: F401
+
+F16, BF16, F32 = 0, 1, 2
+_P, _I32, _I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+
+
+class Rows(ctypes.Structure):
+    """Rows of tokens x heads x columns (mirrors sgemv_rows)."""
+    _fields_ = [("data", _P), ("token_stride", _I64), ("head_stride", _I64),
+                ("tokens", _I32), ("heads", _I32), ("head_dim", _I32), ("dtype", _I32)]
+
+
+class Cache(ctypes.Structure):
+    """A paged cache (mirrors sgemv_cache)."""
+    _fields_ = [("k", _P), ("v", _P), ("k_page", _I64), ("k_slot", _I64), ("k_head", _I64),
+                ("v_page", _I64), ("v_slot", _I64), ("v_head", _I64),
+                ("pages", _I32), ("page_size", _I32), ("heads", _I32), ("head_dim", _I32), ("dtype", _I32)]
+
+
+class Seqs(ctypes.Structure):
+    """Sequences and their new tokens (mirrors sgemv_seqs)."""
+    _fields_ = [("new_start", _P), ("ctx_len", _P), ("pages", _P), ("pages_stride", _I64),
+                ("count", _I32), ("pages_per_seq", _I32)]
+
+
+class RopeArgs(ctypes.Structure):
+    """Rotary positions (mirrors sgemv_rope_t)."""
+    _fields_ = [("turns", _P), ("rot_dim", _I32), ("interleaved", _I32), ("magnitude", ctypes.c_float)]
+
+
+class AttendPlan(ctypes.Structure):
+    """What sgemv_attend enqueues (mirrors sgemv_attend_plan_t)."""
+    _fields_ = [("workspace_bytes", _I64), ("grid", _I64), ("lds_bytes", _I64),
+                ("block", _I32), ("tile_rows", _I32), ("block_keys", _I32), ("splits", _I32)]
+
+    def as_dict(self) -> dict:
+        return {f: getattr(self, f) for f, _ in self._fields_}
+
+
+class Logits(ctypes.Structure):
+    """Penalties, biases and masks on rows of logits (mirrors sgemv_logits)."""
+    _fields_ = [("x", _P), ("out", _P), ("x_stride", _I64), ("out_stride", _I64),
+                ("hist_start", _P), ("hist_ids", _P), ("n_hist", _I64), ("prompt_len", _P),
+                ("repetition", _P), ("frequency", _P), ("presence", _P),
+                ("bias_start", _P), ("bias_ids", _P), ("bias_values", _P), ("n_bias", _I64),
+                ("masks", _P), ("mask_stride", _I64), ("mask_row", _P),
+                ("n_masks", _I32), ("rows", _I32), ("vocab", _I32), ("dtype", _I32), ("out_dtype", _I32)]
+
+
+def rope_table(rot_dim: int, base: float = 10000.0, factor: float = 1.0, context: float = 0.0, low: float = 1.0,
+               high: float = 32.0) -> np.ndarray:
+    """Turns per position of each rotated pair (float64 [rot_dim / 2]); see sgemv_rope_table."""
+    if not 2 <= rot_dim <= 256 or rot_dim % 2:
+        _check(SGEMV_EINVAL, "sgemv_rope_table")
+    out = np.empty(rot_dim // 2, dtype=np.float64)
+    _check(lib().sgemv_rope_table(rot_dim, base, factor, context, low, high, _ptr(out)), "sgemv_rope_table")
+    return out
+
+
+def rope(rope_args: RopeArgs, positions_dev: int, x: Rows, out: Rows, stream: int = 0) -> None:
+    """Enqueue rotary positions alone (raw device pointers in the structures)."""
+    _check(lib().sgemv_rope(_ref(rope_args), positions_dev, _ref(x), _ref(out), stream), "sgemv_rope")
+
+
+def append(cache: Cache, seqs: Seqs, rope_args, positions_dev: int, q, q_out, k: Rows, v: Rows, stream: int = 0) -> None:
+    """Enqueue the append of new tokens to a cache (raw device pointers in the structures; None for what is absent)."""
+    _check(lib().sgemv_append(_ref(cache), _ref(seqs), _ref(rope_args), positions_dev, _ref(q), _ref(q_out), _ref(k), _ref(v), stream), "sgemv_append")
+
+
+def attend_plan(cache: Cache, seqs: Seqs, tokens: int, heads: int, max_ctx: int = 0) -> AttendPlan:
+    """The launch sgemv_attend would make; no GPU needed (device pointers are not read)."""
+    pl = AttendPlan()
+    _check(lib().sgemv_attend_plan(_ref(cache), _ref(seqs), tokens, heads, max_ctx, _ref(pl)), "sgemv_attend_plan")
+    return pl
+
+
+def attend(cache: Cache, seqs: Seqs, q: Rows, out: Rows, scale: float, tree_dev: int = 0, tree_words: int = 0,
+           max_ctx: int = 0, workspace_dev: int = 0, workspace_bytes: int = 0, stream: int = 0) -> None:
+    """Enqueue the attention of new tokens over a cache (raw device pointers)."""
+    _check(lib().sgemv_attend(_ref(cache), _ref(seqs), _ref(q), _ref(out), scale, tree_dev, tree_words, max_ctx, workspace_dev, workspace_bytes,
+                              stream), "sgemv_attend")
+
+
+def _ref(x):
+    return None if x is None else ctypes.byref(x)
+
+
+_types = None
+
+
+def _type(dtype) -> int:
+    global _types
+    if _types is None:
+        import torch
+        _types = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
+    try:
+        return _types[dtype]
+    except KeyError:
+        raise ValueError(f"no operator for {dtype}") from None
+
+
+def _rows(x, what: str) -> Rows:
+    if x.dim() != 3 or x.stride(2) != 1 and x.shape[2] != 1:
+        raise ValueError(f"{what} must be [tokens, heads, head_dim] with contiguous columns")
+    st, sh, _ = x.stride()
+    t, h, d = x.shape
+    return Rows(x.data_ptr(), st, sh, t, h, d, _type(x.dtype))
+
+
+def _on(device, **tensors) -> None:
+    for what, x in tensors.items():
+        if x is not None and x.device != device:
+            raise ValueError(f"{what} is on {x.device}, not on {device}")
+
+
+def _ints(x, what: str, shape=None) -> None:
+    import torch
+    if x.dtype != torch.int32 or not x.is_contiguous() or (shape is not None and tuple(x.shape) != shape):
+        raise ValueError(f"{what} must be a contiguous int32 tensor" + (f" of shape {list(shape)}" if shape is not None else ""))
+
+
+class _Launch:
+    """The device and stream of a call: ``with _Launch(device, stream) as s``
+    makes both current (kernels are launched on the current device, and
+    tensors made inside belong to the stream) and gives the raw stream."""
+    __slots__ = ("device", "stream", "ctx")
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.ctx = device, stream, None
+
+    def __enter__(self) -> int:
+        import torch
+        if self.device.type != "cuda":
+            raise ValueError(f"tensors are on {self.device}, not on a GPU")
+        s = self.stream
+        if s is None:
+            if torch.cuda.current_device() != self.device.index:
+                self.ctx = torch.cuda.device(self.device)
+                self.ctx.__enter__()
+            return torch.cuda.current_stream(self.device).cuda_stream
+        if s.device != self.device:
+            raise ValueError(f"the stream is on {s.device}, the tensors on {self.device}")
+        self.ctx = torch.cuda.stream(s)
+        self.ctx.__enter__()
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+class Rope:
+    """Rotary positions: the frequency table (on ``device``), pairing and magnitude.
+
+    ``factor`` stretches for contexts longer than trained: every frequency
+    divided by it, or, with ``context`` (the trained length), blended by the
+    turns a pair makes over it, from ``low`` (divided) to ``high`` (kept).
+    """
+
+    def __init__(self, rot_dim: int, base: float = 10000.0, interleaved: bool = False, factor: float = 1.0,
+                 context: float = 0.0, low: float = 1.0, high: float = 32.0, magnitude: float = 1.0, device="cuda"):
+        import torch
+        self.turns = torch.from_numpy(rope_table(rot_dim, base, factor, context, low, high)).to(device)
+        self.args = RopeArgs(self.turns.data_ptr(), rot_dim, int(bool(interleaved)), magnitude)
+
+    def apply(self, x, positions, out=None, stream=None):
+        """x [tokens, heads, head_dim] turned at ``positions`` (int32 [tokens]) into ``out`` (a new tensor; x itself is fine)."""
+        import torch
+        _ints(positions, "positions", (x.shape[0],))
+        _on(self.turns.device, x=x, positions=positions, out=out)
+        with _Launch(x.device, stream) as s:
+            if out is None:
+                out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            rope(self.args, positions.data_ptr(), _rows(x, "x"), _rows(out, "out"), s)
+        return out
+
+
+class Sequences:
+    """Sequences and their new tokens, as int32 tensors on the GPU.
+
+    new_start [count + 1]: the first new token of each sequence in the packed
+    rows, and their end; ctx_len [count]: tokens of each sequence, new ones
+    included; pages [count, pages_per_seq]: its pages in the cache. The
+    tensors are read when a kernel runs and may be rewritten between calls.
+    """
+
+    def __init__(self, new_start, ctx_len, pages):
+        import torch
+        count = ctx_len.shape[0]
+        _ints(ctx_len, "ctx_len", (count,))
+        _ints(new_start, "new_start", (count + 1,))
+        if pages.dtype != torch.int32 or pages.dim() != 2 or pages.shape[0] != count or (pages.shape[1] > 1 and pages.stride(1) != 1):
+            raise ValueError("pages must be an int32 tensor of shape [count, pages_per_seq] with contiguous rows")
+        _on(ctx_len.device, new_start=new_start, pages=pages)
+        self.new_start, self.ctx_len, self.pages = new_start, ctx_len, pages
+        self.device = ctx_len.device
+        self.args = Seqs(new_start.data_ptr(), ctx_len.data_ptr(), pages.data_ptr(), pages.stride(0), count, pages.shape[1])
+
+
+class PagedCache:
+    """Keys and values of many sequences in pages of ``page_size`` slots
+    (a power of two, 8 or more): ``k`` and ``v`` are [pages, page_size,
+    heads, head_dim], FP16 or BF16."""
+
+    def __init__(self, pages: int, page_size: int, heads: int, head_dim: int, dtype=None, device="cuda"):
+        import torch
+        shape = (pages, page_size, heads, head_dim)
+        self._set(*(torch.zeros(shape, dtype=dtype or torch.float16, device=device) for _ in range(2)))
+
+    @classmethod
+    def from_tensors(cls, k, v) -> "PagedCache":
+        """A cache over tensors of the caller's, of any strides with
+        contiguous columns (a head-major cache is passed transposed)."""
+        self = cls.__new__(cls)
+        self._set(k, v)
+        return self
+
+    def _set(self, k, v):
+        for what, x in (("k", k), ("v", v)):
+            if x.dim() != 4 or (x.shape[3] > 1 and x.stride(3) != 1):
+                raise ValueError(f"{what} must be [pages, page_size, heads, head_dim] with contiguous columns")
+        if k.shape != v.shape or k.dtype != v.dtype:
+            raise ValueError("k and v differ in shape or type")
+        _on(k.device, v=v)
+        self.k, self.v, self.device = k, v, k.device
+        self.args = Cache(k.data_ptr(), v.data_ptr(), *k.stride()[:3], *v.stride()[:3], *k.shape, _type(k.dtype))
+
+    def append(self, seqs: Sequences, k, v, rope: Rope = None, q=None, q_out=None, positions=None, stream=None):
+        """Store the new tokens' k (turned by ``rope``) and v, [tokens, heads,
+        head_dim], in their slots; q [tokens, query heads, head_dim] turned
+        into ``q_out`` (a new tensor; q itself is fine), which is returned.
+        ``positions`` (int32 [tokens]): instead of the tokens' slots."""
+        import torch
+        if rope is None and (q is not None or positions is not None):
+            raise ValueError("q and positions need a rope")
+        if q is None and q_out is not None:
+            raise ValueError("q_out needs q")
+        if positions is not None:
+            _ints(positions, "positions", (k.shape[0],))
+        _on(self.device, k=k, v=v, q=q, q_out=q_out, positions=positions, seqs=seqs, rope=rope and rope.turns)
+        with _Launch(self.device, stream) as s:
+            if q is not None and q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            append(self.args, seqs.args, rope and rope.args, positions.data_ptr() if positions is not None else 0,
+                   None if q is None else _rows(q, "q"), None if q is None else _rows(q_out, "q_out"),
+                   _rows(k, "k"), _rows(v, "v"), s)
+        return q_out
+
+    def plan(self, seqs: Sequences, tokens: int, heads: int, max_ctx: int = 0) -> AttendPlan:
+        """The launch that ``attend`` would make (its workspace_bytes, its splits)."""
+        return attend_plan(self.args, seqs.args, tokens, heads, max_ctx)
+
+    def attend(self, seqs: Sequences, q, scale: float = None, tree=None, out=None, max_ctx: int = 0, workspace=None,
+               stream=None):
+        """Attention of the new tokens q [tokens, query heads, head_dim] over
+        the cache, which holds them already. scale: 1/sqrt(head_dim) unless
+        given. tree (int32 [tokens, words]): bit j of a row says whether it
+        sees new token j of its sequence; without it a token sees the slots up
+        to its own. max_ctx: the longest context to expect (shapes the launch
+        only). workspace: a uint8 tensor of ``plan(...).workspace_bytes`` or
+        more, not shared with calls that may run at the same time; made if
+        not given. Rows of no sequence stay as they are in a given ``out``
+        and are undefined in a new one."""
+        import torch
+        words = 0
+        if tree is not None:
+            _ints(tree, "tree")
+            if tree.dim() != 2 or tree.shape[0] != q.shape[0]:
+                raise ValueError("tree must be [tokens, words]")
+            words = tree.shape[1]
+        _on(self.device, q=q, seqs=seqs, tree=tree, out=out, workspace=workspace)
+        with _Launch(self.device, stream) as s:
+            if out is None:
+                out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            qr = _rows(q, "q")
+            if workspace is None:
+                need = attend_plan(self.args, seqs.args, qr.tokens, qr.heads, max_ctx).workspace_bytes
+                if need:
+                    workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+            elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+                raise ValueError("workspace must be a contiguous uint8 tensor")
+            attend(self.args, seqs.args, qr, _rows(out, "out"), 1.0 / math.sqrt(q.shape[2]) if scale is None else scale,
+                   tree.data_ptr() if tree is not None else 0, words, max_ctx,
+                   workspace.data_ptr() if workspace is not None else 0, workspace.numel() if workspace is not None else 0, s)
+        return out
+
+
+def adjust_logits(x, out=None, history=None, history_start=None, prompt_len=None, repetition=None, frequency=None,
+                  presence=None, bias_ids=None, bias_values=None, bias_start=None, masks=None, mask_row=None, stream=None):
+    """Penalties, biases and grammar masks on logits x [rows, vocab] (FP16, BF16 or FP32).
+
+    out: x's type or FP32 (a new FP32 tensor unless given; x itself is fine).
+    history (int32, all rows' ids one after the other), history_start (int32
+    [rows + 1]) and prompt_len (int32 [rows]: ids that are the prompt's, for
+    ``repetition`` only); repetition, frequency, presence: float32 [rows];
+    bias_ids, bias_values, bias_start: a ragged list as the history; masks
+    (int32 [n, (vocab + 31) / 32]): bit v of a mask set where token v is
+    allowed; mask_row (int32 [rows]): each row's mask, -1 for none."""
+    import torch
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("x must be [rows, vocab] with contiguous rows")
+    rows, vocab = x.shape
+    if out is not None and (out.shape != x.shape or (vocab > 1 and out.stride(1) != 1)):
+        raise ValueError("out must have the shape of x, and contiguous rows")
+    dev = x.device
+    if (history is None) != (history_start is None):
+        raise ValueError("history and history_start belong together")
+    if (bias_ids is None) != (bias_start is None) or (bias_ids is None) != (bias_values is None):
+        raise ValueError("bias_ids, bias_values and bias_start belong together")
+    g = Logits(x=x.data_ptr(), x_stride=x.stride(0), rows=rows, vocab=vocab, dtype=_type(x.dtype))
+    if history is not None:
+        _on(dev, history=history, history_start=history_start)
+        _ints(history, "history", (history.numel(),))
+        _ints(history_start, "history_start", (rows + 1,))
+        g.hist_ids, g.hist_start, g.n_hist = history.data_ptr(), history_start.data_ptr(), history.numel()
+    if prompt_len is not None:
+        _on(dev, prompt_len=prompt_len)
+        _ints(prompt_len, "prompt_len", (rows,))
+        g.prompt_len = prompt_len.data_ptr()
+    for what, t in (("repetition", repetition), ("frequency", frequency), ("presence", presence)):
+        if t is not None:
+            if t.dtype != torch.float32 or t.shape != (rows,) or not t.is_contiguous() or t.device != dev:
+                raise ValueError(f"{what} must be a contiguous float32 tensor of shape [{rows}] on {dev}")
+            setattr(g, what, t.data_ptr())
+    if bias_ids is not None:
+        _on(dev, bias_ids=bias_ids, bias_start=bias_start, bias_values=bias_values)
+        _ints(bias_ids, "bias_ids", (bias_ids.numel(),))
+        _ints(bias_start, "bias_start", (rows + 1,))
+        if bias_values.dtype != torch.float32 or bias_values.shape != bias_ids.shape or not bias_values.is_contiguous():
+            raise ValueError("bias_values must be a contiguous float32 tensor, one for each of bias_ids")
+        g.bias_ids, g.bias_start, g.bias_values, g.n_bias = (bias_ids.data_ptr(), bias_start.data_ptr(), bias_values.data_ptr(),
+                                                             bias_ids.numel())
+    if masks is not None:
+        _on(dev, masks=masks, mask_row=mask_row)
+        if masks.dtype != torch.int32 or masks.dim() != 2 or masks.shape[1] != (vocab + 31) // 32 or (masks.shape[1] > 1 and masks.stride(1) != 1):
+            raise ValueError(f"masks must be an int32 tensor of shape [n, {(vocab + 31) // 32}] with contiguous rows")
+        g.masks, g.mask_stride, g.n_masks = masks.data_ptr(), masks.stride(0), masks.shape[0]
+        if mask_row is not None:
+            _ints(mask_row, "mask_row", (rows,))
+            g.mask_row = mask_row.data_ptr()
+    elif mask_row is not None:
+        raise ValueError("mask_row needs masks")
+    _on(dev, out=out)
+    with _Launch(dev, stream) as s:
+        if out is None:
+            out = torch.empty(x.shape, dtype=torch.float32, device=dev)
+        g.out, g.out_stride, g.out_dtype = out.data_ptr(), out.stride(0), _type(out.dtype)
+        _check(lib().sgemv_adjust_logits(_ref(g), s), "sgemv_adjust_logits")
+    return out

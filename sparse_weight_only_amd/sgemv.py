@@ -91,7 +91,7 @@ def lib():
                                "(run __graft_entry__.build())")
         L = ctypes.CDLL(_LIB_PATH)
         P = ctypes.c_void_p
-        i32, i64, u32, f64 = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_double
+        i32, i64, u32, f32, f64 = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_float, ctypes.c_double
         D, PL, TK = ctypes.POINTER(Desc), ctypes.POINTER(Plan), ctypes.POINTER(Task)
         LL = ctypes.POINTER(ListLaunch)
         sigs = {
@@ -114,6 +114,12 @@ def lib():
             "sgemv_run_list_table": [P, LL, P],
             "sgemv_probe_read": [P, i64, P, i64, u32, P],
             "sgemv_probe_empty": [i32, i32, P],
+            "sgemv_rope_table": [i32, f64, f64, f64, f64, f64, P],
+            "sgemv_rope": [P, P, P, P, P],
+            "sgemv_append": [P, P, P, P, P, P, P, P, P],
+            "sgemv_attend_plan": [P, P, i32, i32, i32, P],
+            "sgemv_attend": [P, P, P, P, f32, P, i32, i32, P, i64, P],
+            "sgemv_adjust_logits": [P, P],
         }
         for f, argtypes in sigs.items():
             if not hasattr(L, f):
