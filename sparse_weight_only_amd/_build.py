@@ -65,6 +65,7 @@ def build(verbose: bool = False, arch: str = "gfx950") -> str:
     build_c_driver(verbose)
     from . import _build_san
     _build_san.build_host_sanitized(verbose)
+    _build_san.build_index_check(verbose)
     return LIB
 
 

@@ -19,18 +19,13 @@
 
 namespace sgemv_dev {
 
-struct AttendParams {
-  SeqView seq;
+struct AttendParams : TileView {
   const uint16_t *k, *v, *q;
   uint16_t* out;
   int64_t k_page, k_slot, k_head, v_page, v_slot, v_head;
   int64_t q_token, q_head, o_token, o_head;
-  const uint32_t* tree;   // [tokens][tree_words], or null: a token sees the slots up to its own
-  int32_t tree_words;
-  int32_t group;          // query heads per cache head
   int32_t heads;          // cache heads
   int32_t dim;
-  int32_t splits;         // parts of the context, joined by attend_join_kernel
   int32_t slots;          // row tiles, empty ones included
   float scale2;           // scale * log2(e): scores in powers of two
   float* part;            // splits > 1: [row][split][dim] sums, then [row][split] of (m, sum of p)
@@ -93,79 +88,9 @@ __device__ __forceinline__ float max_x16(float x) { const Two t = both_x16(x); r
 __device__ __forceinline__ float sum_x32(float x) { const Two t = both_x32(x); return t.a + t.b; }
 __device__ __forceinline__ float sum_x16(float x) { const Two t = both_x16(x); return t.a + t.b; }
 
-// The rows of a tile are (new token, query head of the group) pairs of one
-// sequence and cache head: row r is token r / group, head r % group, so a
-// tile of a shared head reads its keys once for the whole group.
-//
-// Tiles of M rows are numbered without a pass over the sequences: sequence s
-// has the slots from floor(start(s) group / M) + s on, at least as many as its
-// tiles, since floor(a + b) - floor(a) + 1 >= ceil(b); what is left over is
-// empty. floor(tokens group / M) + count slots in all.
-struct Tile {
-  int s, first, n;          // sequence, its first new token, its new tokens
-  int old;                  // slot of its first new token
-  int row0, rows;           // first row of the tile, rows of the sequence
-  int end, full;            // keys any row sees, keys every row sees
-  int key0, key1;           // this split's part of [0, end)
-  const int32_t* pages;
-};
-
-__device__ __forceinline__ int64_t slot_base(const AttendParams& p, int s, int m) {
-  return (int64_t)p.seq.start(s) * p.group / m + s;
-}
-
-// The keys of the tile at `row0` of sequence t.s, and split `split` of them in
-// whole blocks of `block` keys.
-__device__ __forceinline__ void tile_keys(const AttendParams& p, int m, int block, int split, Tile& t) {
-  const int ctx = p.seq.ctx(t.s);
-  t.old = ctx - t.n;
-  if (p.tree) {
-    t.end = ctx;
-    t.full = t.old;
-  } else {
-    const int last = t.row0 + m < t.rows ? (t.row0 + m - 1) / p.group : t.n - 1;
-    t.end = t.old + last + 1;
-    t.full = t.old + t.row0 / p.group + 1;
-  }
-  t.end = t.end < 0 ? 0 : t.end > ctx ? ctx : t.end;
-  const int blocks = (t.end + block - 1) / block;
-  const int per = (blocks + p.splits - 1) / p.splits * block;
-  const int64_t k0 = (int64_t)split * per;
-  t.key0 = k0 < t.end ? (int)k0 : t.end;
-  t.key1 = k0 + per < t.end ? (int)(k0 + per) : t.end;
-}
-
-__device__ __forceinline__ bool find_tile(const AttendParams& p, int m, int block, int slot, int split, Tile& t) {
-  t.s = wave_upper(p.seq.count, slot, [&](int i) { return slot_base(p, i, m); });
-  t.first = p.seq.start(t.s);
-  t.n = p.seq.start(t.s + 1) - t.first;
-  t.rows = t.n * p.group;
-  const int64_t at = slot - slot_base(p, t.s, m);
-  if (t.n <= 0 || at < 0 || at * m >= t.rows) return false;
-  t.row0 = (int)at * m;
-  t.pages = p.seq.pages + t.s * p.seq.pages_stride;
-  tile_keys(p, m, block, split, t);
-  return true;
-}
-
-// Bit b: whether new token `i` of the tile's sequence sees key kb + b.
-__device__ __forceinline__ uint32_t seen_bits(const AttendParams& p, const Tile& t, int i, int kb) {
-  int n;
-  uint32_t bits = ~0u;
-  if (p.tree) {
-    // the words of this row, from new token kb - old on; older keys are seen
-    const int at = kb - t.old;
-    const uint32_t* w = p.tree + (int64_t)(t.first + i) * p.tree_words;
-    const int w0 = at >> 5, sh = at & 31;      // rounds down for at < 0 too
-    const uint32_t a = w0 < 0 ? ~0u : w0 < p.tree_words ? w[w0] : 0u;
-    const uint32_t b = w0 + 1 < 0 ? ~0u : w0 + 1 < p.tree_words ? w[w0 + 1] : 0u;
-    bits = sh ? (a >> sh) | (b << (32 - sh)) : a;
-    n = t.end - kb;
-  } else {
-    n = t.old + i + 1 - kb;
-    n = n < t.end - kb ? n : t.end - kb;
-  }
-  return n >= 32 ? bits : n <= 0 ? 0u : bits & ((1u << n) - 1u);
+__device__ __forceinline__ bool find_tile(const TileView& p, int m, int block, int slot, int split, Tile& t) {
+  const int s = wave_upper(p.seq.count, slot, [&](int i) { return slot_base(p, i, m); });
+  return make_tile(p, m, block, s, slot, split, t);
 }
 
 __device__ __forceinline__ bool not_finite(float x) { return !(__builtin_fabsf(x) < __builtin_inff()); }

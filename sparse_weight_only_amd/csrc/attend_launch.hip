@@ -52,7 +52,7 @@ int check(const sgemv_cache* cache, const sgemv_seqs* seqs, int32_t tokens, int3
   rc = check_seqs(seqs);
   if (rc) return rc;
   if (tokens < 0 || heads < 1 || heads > 65535 || heads % cache->heads || max_ctx < 0) return SGEMV_EINVAL;
-  return (int64_t)tokens * heads > INT32_MAX ? SGEMV_ESIZE : SGEMV_OK;
+  return (int64_t)tokens * heads > (1 << 30) ? SGEMV_ESIZE : SGEMV_OK;
 }
 
 }  // namespace

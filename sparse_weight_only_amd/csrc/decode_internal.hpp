@@ -19,7 +19,7 @@ inline bool stride_ok(int64_t stride, int64_t n, int64_t least) {
 inline int check_rows(const sgemv_rows* r, bool written) {
   if (!r) return SGEMV_EINVAL;
   if (r->tokens < 0 || r->heads < 1 || r->heads > 65535 || !valid_dim(r->head_dim) || !half_type(r->dtype)) return SGEMV_EINVAL;
-  if ((int64_t)r->tokens * r->heads > INT32_MAX) return SGEMV_ESIZE;
+  if ((int64_t)r->tokens * r->heads > (1 << 30)) return SGEMV_ESIZE;   // rows are counted in 32 bits
   const int64_t least = written ? r->head_dim : 0;
   if (!stride_ok(r->token_stride, r->tokens, least) || !stride_ok(r->head_stride, r->heads, least)) return SGEMV_EINVAL;
   if (r->tokens > 0 && !r->data) return SGEMV_EINVAL;

@@ -119,7 +119,7 @@ def _type(dtype) -> int:
 
 
 def _rows(x, what: str) -> Rows:
-    if x.dim() != 3 or x.stride(2) != 1 and x.shape[2] != 1:
+    if x.dim() != 3 or (x.stride(2) != 1 and x.shape[2] > 1):
         raise ValueError(f"{what} must be [tokens, heads, head_dim] with contiguous columns")
     st, sh, _ = x.stride()
     t, h, d = x.shape
@@ -187,10 +187,11 @@ class Rope:
         import torch
         _ints(positions, "positions", (x.shape[0],))
         _on(self.turns.device, x=x, positions=positions, out=out)
+        xr = _rows(x, "x")
         with _Launch(x.device, stream) as s:
             if out is None:
                 out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-            rope(self.args, positions.data_ptr(), _rows(x, "x"), _rows(out, "out"), s)
+            rope(self.args, positions.data_ptr(), xr, _rows(out, "out"), s)
         return out
 
 
@@ -257,12 +258,12 @@ class PagedCache:
         if positions is not None:
             _ints(positions, "positions", (k.shape[0],))
         _on(self.device, k=k, v=v, q=q, q_out=q_out, positions=positions, seqs=seqs, rope=rope and rope.turns)
+        qr, kr, vr = None if q is None else _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
         with _Launch(self.device, stream) as s:
             if q is not None and q_out is None:
                 q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
             append(self.args, seqs.args, rope and rope.args, positions.data_ptr() if positions is not None else 0,
-                   None if q is None else _rows(q, "q"), None if q is None else _rows(q_out, "q_out"),
-                   _rows(k, "k"), _rows(v, "v"), s)
+                   qr, None if q is None else _rows(q_out, "q_out"), kr, vr, s)
         return q_out
 
     def plan(self, seqs: Sequences, tokens: int, heads: int, max_ctx: int = 0) -> AttendPlan:
@@ -287,17 +288,17 @@ class PagedCache:
             if tree.dim() != 2 or tree.shape[0] != q.shape[0]:
                 raise ValueError("tree must be [tokens, words]")
             words = tree.shape[1]
+        if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
+            raise ValueError("workspace must be a contiguous uint8 tensor")
         _on(self.device, q=q, seqs=seqs, tree=tree, out=out, workspace=workspace)
+        qr = _rows(q, "q")
         with _Launch(self.device, stream) as s:
             if out is None:
                 out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            qr = _rows(q, "q")
             if workspace is None:
                 need = attend_plan(self.args, seqs.args, qr.tokens, qr.heads, max_ctx).workspace_bytes
                 if need:
                     workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
-            elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-                raise ValueError("workspace must be a contiguous uint8 tensor")
             attend(self.args, seqs.args, qr, _rows(out, "out"), 1.0 / math.sqrt(q.shape[2]) if scale is None else scale,
                    tree.data_ptr() if tree is not None else 0, words, max_ctx,
                    workspace.data_ptr() if workspace is not None else 0, workspace.numel() if workspace is not None else 0, s)
