@@ -5,8 +5,11 @@
 // over the visible keys t, in one pass: m is the running maximum of the
 // scores, and what was summed under an older maximum is scaled down when it
 // grows. Scores, m, the sum of the p_t and the output are kept in FP32; p_t is
-// rounded to the cache's type for the second product (half a step of at most
-// 1, the same step as the result's own rounding), its sum is not.
+// rounded to the cache's type for the second product, half a step of its own,
+// as the result is once more. The sum is that of the rounded p_t (a two-way dot
+// product with ones, one operation for two of them), so that a weight that
+// outweighs the others is off in both sums alike. That operation does not
+// round to nearest (its sums were off by up to 2^-21): it adds up a block only.
 //
 // Both products run on the matrix cores, the first transposed (keys x rows),
 // so that a lane holds scores of one row only: the row statistics are a
@@ -20,11 +23,12 @@
 namespace sgemv_dev {
 
 struct AttendParams : TileView {
+  int32_t heads;          // cache heads
   const uint16_t *k, *v, *q;
   uint16_t* out;
-  int64_t k_page, k_slot, k_head, v_page, v_slot, v_head;
+  int64_t k_head, v_head;
+  uint32_t k_page, k_slot, v_page, v_slot;
   int64_t q_token, q_head, o_token, o_head;
-  int32_t heads;          // cache heads
   int32_t dim;
   int32_t slots;          // row tiles, empty ones included
   float scale2;           // scale * log2(e): scores in powers of two
@@ -49,6 +53,10 @@ template <> struct Half<_Float16> {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
   }
   static __device__ __forceinline__ uint32_t pack(float a, float b) { return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b}); }
+  // c + both halves
+  static __device__ __forceinline__ float sum(uint32_t u, float c) {
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, u), f16x2{(_Float16)1.0f, (_Float16)1.0f}, c, false);
+  }
   static __device__ __forceinline__ float lo(uint32_t u) { return (float)__builtin_bit_cast(f16x2, u).x; }
   static __device__ __forceinline__ float hi(uint32_t u) { return (float)__builtin_bit_cast(f16x2, u).y; }
 };
@@ -60,13 +68,41 @@ template <> struct Half<__bf16> {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b16x8, a), __builtin_bit_cast(b16x8, b), c, 0, 0, 0);
   }
   static __device__ __forceinline__ uint32_t pack(float a, float b) { return __builtin_bit_cast(uint32_t, b16x2{(__bf16)a, (__bf16)b}); }
+  static __device__ __forceinline__ float sum(uint32_t u, float c) {
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(b16x2, u), b16x2{(__bf16)1.0f, (__bf16)1.0f}, c, false);
+  }
   static __device__ __forceinline__ float lo(uint32_t u) { return __builtin_bit_cast(float, u << 16); }
   static __device__ __forceinline__ float hi(uint32_t u) { return __builtin_bit_cast(float, u & 0xffff0000u); }
 };
 
-// What lanes read in the place of a key that is not there: V's rows have to
-// be zeros even where their weight is 0 (0 * NaN), K's may be anything.
-static __device__ const dword4 kNothing[2] = {};
+// What lanes read in the place of a key that is not there, as wide as a row:
+// V's rows have to be zeros even where their weight is 0 (0 * NaN), K's may be
+// anything.
+static __device__ const dword4 kNothing[32] = {};
+
+// Addresses as whole numbers, so that choosing between a key and nothing is a
+// select and not a branch around a load, and loads know that they are global.
+typedef uint64_t addr_t;
+__device__ __forceinline__ addr_t addr(const void* p) { return (addr_t)p; }
+// `a` where it is there. What `a` is computed from is hidden, or the compiler
+// would branch around the arithmetic instead of selecting.
+__device__ __forceinline__ addr_t or_nothing(bool there, addr_t a) {
+  asm("" : "+v"(a));
+  return there ? a : addr(kNothing);
+}
+template <class V>
+__device__ __forceinline__ V load(addr_t a) { return *(const __attribute__((address_space(1))) V*)a; }
+
+// Element `slot` rows into page `page` of a cache whose strides fit 32 bits.
+__device__ __forceinline__ uint64_t element(int page, uint32_t page_stride, int slot, uint32_t slot_stride) {
+  return (uint64_t)(uint32_t)page * page_stride + (uint64_t)(uint32_t)slot * slot_stride;
+}
+
+// The running maximum is raised only when a score passes it by more than this
+// (in powers of two): the sums are then scaled down, a pass over the whole
+// output, for a few blocks instead of most. Weights reach 2^8 at most, as
+// exact in either type as those up to 1.
+constexpr float kSlack = 8.0f;
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 // max and sum with the lane 16 or 32 places away
@@ -88,9 +124,21 @@ __device__ __forceinline__ float max_x16(float x) { const Two t = both_x16(x); r
 __device__ __forceinline__ float sum_x32(float x) { const Two t = both_x32(x); return t.a + t.b; }
 __device__ __forceinline__ float sum_x16(float x) { const Two t = both_x16(x); return t.a + t.b; }
 
-__device__ __forceinline__ bool find_tile(const TileView& p, int m, int block, int slot, int split, Tile& t) {
-  const int s = wave_upper(p.seq.count, slot, [&](int i) { return slot_base(p, i, m); });
-  return make_tile(p, m, block, s, slot, split, t);
+// The tile of a workgroup. Up to 64 sequences: every lane reads one's lengths,
+// so that one round trip to memory gives all there is to know.
+template <int M>
+__device__ __forceinline__ bool find_tile(const TileView& p, int block, int slot, int split, Tile& t) {
+  const int count = p.seq.count;
+  if (count <= 64) {
+    const int lane = threadIdx.x & 63, i = lane < count ? lane : count - 1;
+    const int first = p.seq.start(i), next = p.seq.start(i + 1), ctx = p.seq.ctx(i);
+    const int holds = __popcll(__ballot(lane < count && slot_base(p, i, first, M) <= slot));
+    const int s = holds < 1 ? 0 : holds - 1;
+    return make_tile(p, M, block, s, __builtin_amdgcn_readlane(first, s), __builtin_amdgcn_readlane(next, s),
+                     __builtin_amdgcn_readlane(ctx, s), slot, split, t);
+  }
+  const int s = wave_upper(count, slot, [&](int i) { return slot_base(p, i, p.seq.start(i), M); });
+  return make_tile(p, M, block, s, p.seq.start(s), p.seq.start(s + 1), p.seq.ctx(s), slot, split, t);
 }
 
 __device__ __forceinline__ bool not_finite(float x) { return !(__builtin_fabsf(x) < __builtin_inff()); }

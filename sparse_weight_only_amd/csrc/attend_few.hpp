@@ -4,9 +4,9 @@
 
 namespace sgemv_dev {
 
-constexpr int kFewRows = 16, kFewBlock = 32, kFewWaves = 4;
+constexpr int kFewRows = 16, kFewBlock = 32;
 
-// One workgroup: a tile of 16 rows and one split of its keys; its 4 waves
+// One workgroup: a tile of 16 rows and one split of its keys; its W waves
 // take blocks of 32 keys in turn and meet in LDS at the end. Bound by reading
 // K and V once: the operands come straight from memory, 16 bytes a lane, in
 // the order the matrix cores want them, with the next block's loads in flight.
@@ -14,7 +14,7 @@ constexpr int kFewRows = 16, kFewBlock = 32, kFewWaves = 4;
 //   V^T (16 columns x 32 keys): lane r + 16 g has the keys of group g and the
 //   columns DP/16 r .., so a load is again one row's run, and a step for
 //   column c of each run is put together from two rows at a time (v_perm).
-template <class T, int DP>
+template <class T, int DP, bool WHOLE, int W>
 struct Few {
   static constexpr int KC = DP / 32;      // K steps: 16-byte pieces of a key in a lane
   static constexpr int VC = DP / 16;      // columns of V in a lane = 16-column tiles of the output
@@ -47,13 +47,17 @@ struct Few {
 #pragma unroll
     for (int c = 0; c < KC; ++c) {
       const int d = 32 * c + 8 * g;
-      q[c] = d < p.dim ? *(const dword4*)(qr + d) : dword4{0, 0, 0, 0};
+      q[c] = columns<dword4>(addr(qr), d);
     }
   }
 
-  __device__ __forceinline__ int page_of(int key) const {
-    return key < t.key1 ? t.pages[key >> p.seq.page_shift] : -1;
+  // columns d .. of a row; zeros past the head's own where it is narrower than DP
+  template <class V>
+  __device__ __forceinline__ V columns(addr_t row, int d) const {
+    return load<V>(WHOLE ? row + 2 * d : or_nothing(d < p.dim, row + 2 * d));
   }
+  // a key past the end looks up the last one's page
+  __device__ __forceinline__ int page_of(int key) const { return t.pages[(key < t.key1 ? key : t.key1 - 1) >> p.seq.page_shift]; }
   __device__ __forceinline__ Rows lookup(int kb) const {
     Rows w;
 #pragma unroll
@@ -63,7 +67,7 @@ struct Few {
     }
     return w;
   }
-  __device__ __forceinline__ void load(int kb, const Rows& w, Block& b) const {
+  __device__ __forceinline__ void fetch(int kb, const Rows& w, Block& b) const {
     const int in_page = (1 << p.seq.page_shift) - 1;
     uint32_t there = 0;
 #pragma unroll
@@ -71,28 +75,24 @@ struct Few {
       const int key = kb + 16 * i + r;
       const bool ok = key < t.key1 && p.seq.page_ok(w.k[i]);
       there |= (uint32_t)(__ballot(ok) & 0xffffu) << (16 * i);
-      const uint16_t* row = kh + w.k[i] * p.k_page + (key & in_page) * p.k_slot;
+      const addr_t row = or_nothing(ok, addr(kh + element(w.k[i], p.k_page, key & in_page, p.k_slot)));
 #pragma unroll
-      for (int c = 0; c < KC; ++c) {
-        const int d = 32 * c + 8 * g;
-        b.k[i][c] = *(ok && d < p.dim ? (const dword4*)(row + d) : kNothing);
-      }
+      for (int c = 0; c < KC; ++c) b.k[i][c] = columns<dword4>(row, 32 * c + 8 * g);
     }
     b.there = there;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int key = kb + 16 * (j / 4) + 4 * g + j % 4;
       const bool ok = key < t.key1 && p.seq.page_ok(w.v[j / 4]);
-      const uint16_t* row = vh + w.v[j / 4] * p.v_page + (key & in_page) * p.v_slot;
+      const addr_t row = or_nothing(ok, addr(vh + element(w.v[j / 4], p.v_page, key & in_page, p.v_slot)));
       if constexpr (VC == 4) {
-        const dword2 x = *(ok && 4 * r < p.dim ? (const dword2*)(row + 4 * r) : (const dword2*)kNothing);
+        const dword2 x = columns<dword2>(row, 4 * r);
         b.v[j][0] = x.x;
         b.v[j][1] = x.y;
       } else {
 #pragma unroll
         for (int u = 0; u < VC / 8; ++u) {
-          const int d = VC * r + 8 * u;
-          const dword4 x = *(ok && d < p.dim ? (const dword4*)(row + d) : kNothing);
+          const dword4 x = columns<dword4>(row, VC * r + 8 * u);
 #pragma unroll
           for (int e = 0; e < 4; ++e) b.v[j][4 * u + e] = x[e];
         }
@@ -124,7 +124,7 @@ struct Few {
     scores(kb, b, s);
     float top = fmaxf(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])), fmaxf(fmaxf(s[4], s[5]), fmaxf(s[6], s[7])));
     top = max_x32(max_x16(top)) * p.scale2;
-    if (__any(top > m)) {
+    if (__any(top > m + kSlack)) {
       const float to = fmaxf(m, top), by = m == to ? 1.0f : exp2_fast(m - to);
       l *= by;
 #pragma unroll
@@ -132,13 +132,14 @@ struct Few {
       m = to;
     }
     const float base = m == -__builtin_inff() ? 0.0f : m;
-    float pr[8];
+    dword4 pb;
+    float sum = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      pr[e] = exp2_fast(__builtin_fmaf(s[e], p.scale2, -base));
-      l += pr[e];
+    for (int e = 0; e < 4; ++e) {
+      pb[e] = Half<T>::pack(exp2_fast(__builtin_fmaf(s[2 * e], p.scale2, -base)), exp2_fast(__builtin_fmaf(s[2 * e + 1], p.scale2, -base)));
+      sum = Half<T>::sum(pb[e], sum);
     }
-    const dword4 pb = {Half<T>::pack(pr[0], pr[1]), Half<T>::pack(pr[2], pr[3]), Half<T>::pack(pr[4], pr[5]), Half<T>::pack(pr[6], pr[7])};
+    l += sum;
 #pragma unroll
     for (int u = 0; u < VD; ++u) {
       dword4 lo, hi;
@@ -157,7 +158,7 @@ struct Few {
   // is infinite or not a number. Only for a tile whose sums are not finite.
   __device__ __forceinline__ void add_seen_only(int kb) {
     Block b;
-    load(kb, lookup(kb), b);
+    fetch(kb, lookup(kb), b);
     float s[8];
     scores(kb, b, s);
     const float base = m == -__builtin_inff() ? 0.0f : m;
@@ -169,7 +170,7 @@ struct Few {
       const float sk = __shfl(key < 16 ? s0 : s1, from);
       if (!(b.there >> key & 1u)) continue;
       const int page = t.pages[(kb + key) >> p.seq.page_shift];
-      const uint16_t* row = vh + page * p.v_page + ((kb + key) & ((1 << p.seq.page_shift) - 1)) * p.v_slot;
+      const uint16_t* row = vh + element(page, p.v_page, (kb + key) & ((1 << p.seq.page_shift) - 1), p.v_slot);
       if (sk == -__builtin_inff()) continue;
       const float pk = exp2_fast(__builtin_fmaf(sk, p.scale2, -base));
 #pragma unroll
@@ -178,7 +179,7 @@ struct Few {
         for (int u = 0; u < VD; ++u) {
           const int d = (4 * g + e4) * VC + 2 * u;
           if (d >= p.dim) continue;
-          const uint32_t w = *(const uint32_t*)(row + d);
+          const uint32_t w = load<uint32_t>(addr(row + d));
           o[2 * u][e4] += pk * Half<T>::lo(w);
           o[2 * u + 1][e4] += pk * Half<T>::hi(w);
         }
@@ -195,20 +196,22 @@ struct Few {
     m = -__builtin_inff();
     l = 0.0f;
     clear();
-    constexpr int step = kFewBlock * kFewWaves;
+    constexpr int step = kFewBlock * W;
     int kb = t.key0 + wave * kFewBlock;
     if (kb < t.key1) {
       Block a, b;
-      Rows w = lookup(kb);
-      load(kb, w, a);
-      w = lookup(kb + step);
+      // pages are looked up two blocks ahead, before the loads of the next
+      // block: loads return in order, so one that was issued later could not
+      // be waited for without waiting for that block too
+      Rows w = lookup(kb), next = lookup(kb + step);
+      fetch(kb, w, a);
       while (true) {
-        load(kb + step, w, b);
         w = lookup(kb + 2 * step);
+        fetch(kb + step, next, b);
         add(kb, a);
         if ((kb += step) >= t.key1) break;
-        load(kb + step, w, a);
-        w = lookup(kb + 2 * step);
+        next = lookup(kb + 2 * step);
+        fetch(kb + step, w, a);
         add(kb, b);
         if ((kb += step) >= t.key1) break;
       }
@@ -226,17 +229,18 @@ struct Few {
   }
 };
 
-template <class T, int DP>
-__global__ void __launch_bounds__(64 * kFewWaves) attend_few_kernel(AttendParams p) {
+template <class T, int DP, bool WHOLE, int W>
+__global__ void __launch_bounds__(64 * W, DP == 256 ? 1 : 2) attend_few_kernel(AttendParams p) {
   constexpr int VC = DP / 16;
-  __shared__ float sums[kFewWaves][kFewRows][DP + 4];
-  __shared__ float stat_m[kFewWaves][kFewRows], stat_l[kFewWaves][kFewRows];
+  __shared__ float sums[W][kFewRows][DP + 4];
+  __shared__ float stat_m[W][kFewRows], stat_l[W][kFewRows];
   const int id = blockIdx.x, head = id % p.heads, split = id / p.heads % p.splits, slot = id / p.heads / p.splits;
   Tile t;
-  if (!find_tile(p, kFewRows, kFewBlock, slot, split, t)) return;
+  if (!find_tile<kFewRows>(p, kFewBlock, slot, split, t)) return;
+  if (p.splits > 1 && t.key0 >= t.key1) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   {
-    Few<T, DP> f(p, t, head);
+    Few<T, DP, WHOLE, W> f(p, t, head);
     f.walk(wave);
     if (f.g == 0) {
       stat_m[wave][f.r] = f.m;
@@ -249,15 +253,16 @@ __global__ void __launch_bounds__(64 * kFewWaves) attend_few_kernel(AttendParams
         *(f32x4*)&sums[wave][f.r][(4 * f.g + e) * VC + c] = f32x4{f.o[c][e], f.o[c + 1][e], f.o[c + 2][e], f.o[c + 3][e]};
   }
   __syncthreads();
-  // 16 lanes a row, 8 columns at a time
-  const int row = threadIdx.x >> 4, r = t.row0 + row;
+  // 4 W lanes a row
+  constexpr int PER = 4 * W;
+  const int row = threadIdx.x / PER, at_row = threadIdx.x % PER, r = t.row0 + row;
   if (r >= t.rows) return;
   float top = -__builtin_inff();
 #pragma unroll
-  for (int w = 0; w < kFewWaves; ++w) top = fmaxf(top, stat_m[w][row]);
-  float by[kFewWaves], l = 0.0f;
+  for (int w = 0; w < W; ++w) top = fmaxf(top, stat_m[w][row]);
+  float by[W], l = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kFewWaves; ++w) {
+  for (int w = 0; w < W; ++w) {
     // a wave without a visible key has sums of zero (or, seeing keys whose
     // scores are not numbers, sums that have to stay so)
     by[w] = stat_m[w][row] == top ? 1.0f : exp2_fast(stat_m[w][row] - top);
@@ -265,30 +270,20 @@ __global__ void __launch_bounds__(64 * kFewWaves) attend_few_kernel(AttendParams
   }
   const int tok = t.first + r / p.group, hq = head * p.group + r % p.group;
   const int64_t at = (int64_t)tok * p.heads * p.group + hq;
-  if (p.splits > 1 && t.key0 < t.key1 && (threadIdx.x & 15) == 0) {
+  if (p.splits > 1 && at_row == 0) {
     float* st = part_stats(p, at, split);
     st[0] = top;
     st[1] = l;
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  for (int d = (threadIdx.x & 15) * 8; d < p.dim; d += 128) {
-    float x[8];
+  for (int d = at_row * 4; d < p.dim; d += PER * 4) {
+    f32x4 x = {0, 0, 0, 0};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x[e] = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kFewWaves; ++w) x[e] += by[w] * sums[w][row][d + e];
-    }
-    if (p.splits > 1) {
-      if (t.key0 >= t.key1) continue;
-      float* to = part_sums(p, at, split) + d;
-      *(f32x4*)to = f32x4{x[0], x[1], x[2], x[3]};
-      *(f32x4*)(to + 4) = f32x4{x[4], x[5], x[6], x[7]};
-    } else {
-      *(dword4*)(p.out + tok * p.o_token + hq * p.o_head + d) =
-          dword4{Half<T>::pack(x[0] * inv, x[1] * inv), Half<T>::pack(x[2] * inv, x[3] * inv),
-                 Half<T>::pack(x[4] * inv, x[5] * inv), Half<T>::pack(x[6] * inv, x[7] * inv)};
-    }
+    for (int w = 0; w < W; ++w) x += by[w] * *(const f32x4*)&sums[w][row][d];
+    if (p.splits > 1)
+      *(f32x4*)(part_sums(p, at, split) + d) = x;
+    else
+      *(dword2*)(p.out + tok * p.o_token + hq * p.o_head + d) = dword2{Half<T>::pack(x[0] * inv, x[1] * inv), Half<T>::pack(x[2] * inv, x[3] * inv)};
   }
 }
 

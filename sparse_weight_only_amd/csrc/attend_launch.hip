@@ -1,5 +1,7 @@
 // sgemv_attend_plan / sgemv_attend: host checks and the launches of the attention.
+#include "attend_join.hpp"
 #include "attend_kernels.hpp"
+#include "attend_many.hpp"
 #include "decode_internal.hpp"
 #include "launch_util.hpp"
 
@@ -9,12 +11,12 @@ using sgemv_dev::AttendParams;
 namespace {
 
 constexpr int kCus = 256;
-constexpr int kMaxSplits = 256;
+using sgemv_dev::kMaxSplits;
 
 struct Shape {
-  bool few;
+  bool few, halves;
   int dp, tile_rows, block, waves, splits;
-  int64_t lds, slots, workspace;
+  int64_t lds, slots, grid, workspace;
 };
 
 // Which kernel, and in how many parts the context is split: from the sizes on
@@ -24,24 +26,37 @@ int make_shape(const sgemv_cache* c, const sgemv_seqs* s, int32_t tokens, int32_
   Shape h;
   h.dp = c->head_dim <= 64 ? 64 : c->head_dim <= 128 ? 128 : 256;
   const int64_t rows = (int64_t)tokens * group;
+  // Up to 32 rows a sequence on average: tiles of 16 rows that read K and V
+  // straight from memory, each tile for itself (27 candidates of 4 heads, 108
+  // rows: 55 us as 7 such tiles, 34 as one of 128). Up to 128: the tiles of 128.
   h.few = rows <= (int64_t)32 * s->count;
-  h.waves = h.few || h.dp == 256 ? 4 : 8;
-  h.tile_rows = h.few ? 16 : 32 * h.waves;
-  h.block = h.few ? 32 : 64;
-  h.lds = h.few ? 0 : (int64_t)2 * 2 * 64 * h.dp * 2;
+  h.waves = h.few ? (h.dp == 256 ? 4 : 8) : sgemv_dev::kManyWaves;
+  h.halves = !h.few && h.dp < 256 && rows <= (int64_t)128 * s->count;
+  h.tile_rows = h.few ? 16 : h.halves ? sgemv_dev::kManyRows<true> : sgemv_dev::kManyRows<false>;
+  h.block = h.few || h.dp == 256 ? 32 : 64;
+  h.lds = h.few ? 0 : h.dp == 64 ? sgemv_dev::kManyLds<64> : h.dp == 128 ? sgemv_dev::kManyLds<128> : sgemv_dev::kManyLds<256>;
   h.slots = rows / h.tile_rows + s->count;
   int64_t ctx = (int64_t)s->pages_per_seq * c->page_size;
   if (max_ctx > 0 && max_ctx < ctx) ctx = max_ctx;
   int64_t tiles = (rows + h.tile_rows - 1) / h.tile_rows;
   const int64_t each = s->count < tokens ? s->count : tokens;
-  if (tiles < each) tiles = each;
-  const int64_t want = 2 * kCus / (tiles * c->heads);
-  const int64_t most = ctx / 256;
+  tiles = tiles < each ? each : tiles;
+  // Workgroups to aim for: one a compute unit, as a workgroup has eight waves
+  // and up to 128 KiB of LDS; two of the 64-column kernel fit (a chunk of 777
+  // and one of 544 over up to 9001: 71 us, 76 with one). More parts than that
+  // only add to what is joined (131071 slots, 8 heads: 100 us with 256, 102
+  // with 512, 107 with 1024). A part has two blocks at least in the few-row
+  // kernel (700 slots, 32 heads: 10.0 us with parts of 64, 11.0 of 128, 12.8
+  // of 256), four in the other.
+  const int64_t want = (!h.few && h.dp == 64 ? 2 : 1) * kCus / (tiles * c->heads);
+  const int64_t most = ctx / (h.few ? 64 : 256);
   int64_t splits = want < most ? want : most;
   splits = splits < 1 ? 1 : splits > kMaxSplits ? kMaxSplits : splits;
   h.splits = (int)splits;
   h.workspace = splits > 1 ? (int64_t)tokens * heads * splits * (c->head_dim + 2) * 4 : 0;
-  if (h.slots * c->heads * splits * h.waves * 64 > (int64_t)UINT32_MAX) return SGEMV_ESIZE;
+  h.grid = h.slots * c->heads * splits;
+  if (h.grid * h.waves * 64 > (int64_t)UINT32_MAX) return SGEMV_ESIZE;   // lanes of a grid axis fit 32 bits
+  if (splits > 1 && (int64_t)tokens * heads * 256 > (int64_t)UINT32_MAX) return SGEMV_ESIZE;
   *out = h;
   return SGEMV_OK;
 }
@@ -51,6 +66,9 @@ int check(const sgemv_cache* cache, const sgemv_seqs* seqs, int32_t tokens, int3
   if (rc) return rc;
   rc = check_seqs(seqs);
   if (rc) return rc;
+  // the kernels' page and slot strides, and eight slots' bytes, fit 32 bits
+  for (const int64_t* d : {&cache->k_page, &cache->v_page})
+    if ((cache->pages > 1 && d[0] > INT32_MAX) || d[1] > INT32_MAX / 16) return SGEMV_ESIZE;
   if (tokens < 0 || heads < 1 || heads > 65535 || heads % cache->heads || max_ctx < 0) return SGEMV_EINVAL;
   return (int64_t)tokens * heads > (1 << 30) ? SGEMV_ESIZE : SGEMV_OK;
 }
@@ -69,7 +87,7 @@ extern "C" int sgemv_attend_plan(const sgemv_cache* cache, const sgemv_seqs* seq
     const int rs = make_shape(cache, seqs, tokens, heads, max_ctx, &h);
     if (rs) return rs;
     q.workspace_bytes = h.workspace;
-    q.grid = h.slots * cache->heads * h.splits;
+    q.grid = h.grid;
     q.lds_bytes = h.lds;
     q.block = 64 * h.waves;
     q.tile_rows = h.tile_rows;
@@ -109,10 +127,10 @@ extern "C" int sgemv_attend(const sgemv_cache* cache, const sgemv_seqs* seqs, co
   p.v = (const uint16_t*)cache->v;
   p.q = (const uint16_t*)q->data;
   p.out = (uint16_t*)out->data;
-  p.k_page = cache->pages > 1 ? cache->k_page : 0;
-  p.v_page = cache->pages > 1 ? cache->v_page : 0;
-  p.k_slot = cache->k_slot;
-  p.v_slot = cache->v_slot;
+  p.k_page = cache->pages > 1 ? (uint32_t)cache->k_page : 0;
+  p.v_page = cache->pages > 1 ? (uint32_t)cache->v_page : 0;
+  p.k_slot = (uint32_t)cache->k_slot;
+  p.v_slot = (uint32_t)cache->v_slot;
   p.k_head = cache->heads > 1 ? cache->k_head : 0;
   p.v_head = cache->heads > 1 ? cache->v_head : 0;
   p.q_token = q->tokens > 1 ? q->token_stride : 0;
@@ -129,15 +147,19 @@ extern "C" int sgemv_attend(const sgemv_cache* cache, const sgemv_seqs* seqs, co
   p.scale2 = scale * 1.44269504088896340736f;
   p.part = (float*)workspace_dev;
   const bool bf16 = q->dtype == SGEMV_BF16;
-  sgemv_dev::AttendFn fn = h.few ? sgemv_dev::get_attend_few(bf16, h.dp) : sgemv_dev::get_attend_many(bf16, h.dp);
+  sgemv_dev::AttendFn fn = h.few ? sgemv_dev::get_attend_few(bf16, p.dim, h.waves) : sgemv_dev::get_attend_many(bf16, p.dim, h.halves);
   (void)hipGetLastError();
   if (ensure_lds((const void*)fn, h.lds)) return SGEMV_EHIP;
-  hipLaunchKernelGGL(fn, dim3((uint32_t)(h.slots * cache->heads * h.splits)), dim3(64 * h.waves), (uint32_t)h.lds, (hipStream_t)hip_stream, p);
+  hipLaunchKernelGGL(fn, dim3((uint32_t)h.grid), dim3(64 * h.waves), (uint32_t)h.lds, (hipStream_t)hip_stream, p);
   if (hipGetLastError() != hipSuccess) return SGEMV_EHIP;
   if (h.splits > 1) {
     const int64_t rows = (int64_t)q->tokens * q->heads;
-    hipLaunchKernelGGL(sgemv_dev::get_attend_join(bf16), dim3((uint32_t)((rows + 3) / 4)), dim3(256), 0, (hipStream_t)hip_stream, p,
-                       h.tile_rows, h.block);
+    // a workgroup a row while that fills the chip a few times over at most,
+    // then DP/4 lanes a row
+    const bool many = rows >= 4 * kCus;
+    const int64_t grid = many ? (rows * (h.dp / 4) + sgemv_dev::kJoinLanes - 1) / sgemv_dev::kJoinLanes : rows;
+    hipLaunchKernelGGL(sgemv_dev::get_attend_join(bf16, p.dim, many), dim3((uint32_t)grid), dim3(sgemv_dev::kJoinLanes), 0,
+                       (hipStream_t)hip_stream, p, h.tile_rows, h.block);
     if (hipGetLastError() != hipSuccess) return SGEMV_EHIP;
   }
   return SGEMV_OK;

@@ -13,7 +13,7 @@ typedef uint32_t dword4 __attribute__((ext_vector_type(4)));
 // f(0) <= x (0 otherwise): each step the wave's 64 lanes look at 64 places,
 // so one round trip finds one of up to 64 sequences and two one of 4096.
 template <class F>
-__device__ __forceinline__ int wave_upper(int count, int64_t x, F f) {
+__device__ __forceinline__ int wave_upper(int count, int x, F f) {
   const int lane = threadIdx.x & 63;
   Upper u(count);
   while (u.n > 1) u.narrow(__popcll(__ballot(u.in(lane) && f(u.place(lane)) <= x)));

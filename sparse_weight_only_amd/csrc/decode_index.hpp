@@ -75,14 +75,15 @@ struct Tile {
   const int32_t* pages;
 };
 
-SGEMV_BOTH int64_t slot_base(const TileView& p, int s, int m) {
-  return (int64_t)p.seq.start(s) * p.group / m + s;
+// First slot of sequence s, whose first new token is `first`. tokens x heads
+// is at most 2^30, so rows fit 32 bits without a sign.
+SGEMV_BOTH int slot_base(const TileView& p, int s, int first, int m) {
+  return (int)((uint32_t)first * (uint32_t)p.group / (uint32_t)m) + s;
 }
 
 // The keys of the tile at `row0` of sequence t.s, and split `split` of them in
 // whole blocks of `block` keys.
-SGEMV_BOTH void tile_keys(const TileView& p, int m, int block, int split, Tile& t) {
-  const int ctx = p.seq.ctx(t.s);
+SGEMV_BOTH void tile_keys(const TileView& p, int m, int block, int ctx, int split, Tile& t) {
   t.old = ctx - t.n;
   if (p.tree) {
     t.end = ctx;
@@ -100,17 +101,18 @@ SGEMV_BOTH void tile_keys(const TileView& p, int m, int block, int split, Tile& 
   t.key1 = k0 + per < t.end ? (int)(k0 + per) : t.end;
 }
 
-// The tile of `slot`, which lies in sequence s; false for an empty slot.
-SGEMV_BOTH bool make_tile(const TileView& p, int m, int block, int s, int slot, int split, Tile& t) {
+// The tile of `slot`, which lies in sequence s with new tokens first .. next - 1
+// and ctx tokens in all; false for an empty slot.
+SGEMV_BOTH bool make_tile(const TileView& p, int m, int block, int s, int first, int next, int ctx, int slot, int split, Tile& t) {
   t.s = s;
-  t.first = p.seq.start(t.s);
-  t.n = p.seq.start(t.s + 1) - t.first;
+  t.first = first;
+  t.n = next - first;
   t.rows = t.n * p.group;
-  const int64_t at = slot - slot_base(p, t.s, m);
+  const int64_t at = slot - slot_base(p, s, first, m);
   if (t.n <= 0 || at < 0 || at * m >= t.rows) return false;
   t.row0 = (int)at * m;
-  t.pages = p.seq.pages + t.s * p.seq.pages_stride;
-  tile_keys(p, m, block, split, t);
+  t.pages = p.seq.pages + s * p.seq.pages_stride;
+  tile_keys(p, m, block, ctx, split, t);
   return true;
 }
 

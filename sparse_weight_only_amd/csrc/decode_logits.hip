@@ -38,20 +38,60 @@ using Four = T __attribute__((ext_vector_type(4), aligned(sizeof(T))));   // row
 
 __device__ __forceinline__ int64_t clamp64(int64_t v, int64_t most) { return v < 0 ? 0 : v > most ? most : v; }
 
+// f(entry, place) for the ids of a list that fall into the part; eight ids of
+// a lane are on their way at once.
+template <class F>
+__device__ __forceinline__ void each_id(const int32_t* ids, int64_t a, int64_t b, int v0, int n, F f) {
+  constexpr int AHEAD = 8;
+  for (int64_t i0 = a + threadIdx.x; i0 < b; i0 += kLanes * AHEAD) {
+    int32_t id[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int64_t i = i0 + k * kLanes;
+      id[k] = ids[i < b ? i : b - 1];
+    }
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int64_t i = i0 + k * kLanes;
+      const uint32_t at = (uint32_t)id[k] - (uint32_t)v0;
+      if (i < b && at < (uint32_t)n) f(at, i);
+    }
+  }
+}
+
 // Workgroup (c, b): entries c kPart .. of row b. The counts of its entries are
 // kept in LDS: every lane walks the history and counts the ids that fall into
-// the part (whole numbers, so the order of the atomics does not matter); of a
-// bias id given twice the later place wins, by an atomic maximum of the places.
+// the part (whole numbers, so the order of the atomics does not matter). Of a
+// bias id given twice the later place wins, by an atomic maximum of the places;
+// then the winners put their values where the places were.
+// Bound by memory for a batch, by its round trips for one row: everything that
+// does not wait for something else is asked for at the start.
 template <class TI, class TO, bool HIST, bool BIAS>
 __global__ void __launch_bounds__(kLanes) logits_kernel(LogitsParams p) {
   __shared__ uint32_t count[HIST ? kPart : 1];       // bit 31: in the prompt; below: how often behind it
-  __shared__ uint32_t place[BIAS ? kPart : 1];       // place in the row's bias list + 1
+  __shared__ uint32_t place[BIAS ? kPart : 1];       // place in the row's bias list + 1, then the bias
   const int tid = threadIdx.x, row = blockIdx.y;
   const int v0 = blockIdx.x * kPart;
   const int n = p.vocab - v0 < kPart ? p.vocab - v0 : kPart;
   const TI* x = (const TI*)p.x + row * p.x_stride + v0;
   TO* out = (TO*)p.out + row * p.out_stride + v0;
 
+  int64_t h0 = 0, h1 = 0, b0 = 0, b1 = 0;
+  int prompt = 0, m = -1;
+  float rep = 1.0f, freq = 0.0f, pres = 0.0f;
+  if (HIST) {
+    h0 = p.hist_start[row];
+    h1 = p.hist_start[row + 1];
+    if (p.prompt_len) prompt = p.prompt_len[row];
+    if (p.repetition) rep = p.repetition[row];
+    if (p.frequency) freq = p.frequency[row];
+    if (p.presence) pres = p.presence[row];
+  }
+  if (BIAS) {
+    b0 = p.bias_start[row];
+    b1 = p.bias_start[row + 1];
+  }
+  if (p.masks) m = p.mask_row ? p.mask_row[row] : row;
   float l[kSteps][kPer];
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
@@ -65,6 +105,13 @@ __global__ void __launch_bounds__(kLanes) logits_kernel(LogitsParams p) {
       for (int e = 0; e < kPer; ++e) l[s][e] = at + e < n ? (float)x[at + e] : 0.0f;
     }
   }
+  uint32_t allowed[kSteps];
+  const bool masked = (uint32_t)m < (uint32_t)p.n_masks;
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    const int at = (s * kLanes + tid) * kPer;
+    allowed[s] = masked && at < n ? p.masks[m * p.mask_stride + ((v0 + at) >> 5)] >> (at & 31) : ~0u;
+  }
   if (HIST || BIAS) {
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
@@ -73,41 +120,54 @@ __global__ void __launch_bounds__(kLanes) logits_kernel(LogitsParams p) {
     }
     __syncthreads();
   }
-  float rep = 1.0f, freq = 0.0f, pres = 0.0f;
   if (HIST) {
-    const int64_t a = clamp64(p.hist_start[row], p.n_hist), b = clamp64(p.hist_start[row + 1], p.n_hist);
-    const int64_t prompt = a + (p.prompt_len ? p.prompt_len[row] : 0);
-    if (p.repetition) rep = p.repetition[row];
-    if (p.frequency) freq = p.frequency[row];
-    if (p.presence) pres = p.presence[row];
-    for (int64_t i = a + tid; i < b; i += kLanes) {
-      const uint32_t id = (uint32_t)(p.hist_ids[i] - v0);
-      if (id < (uint32_t)n) {
-        if (i < prompt) atomicOr(&count[id], 0x80000000u);
-        else atomicAdd(&count[id], 1u);
-      }
-    }
+    h0 = clamp64(h0, p.n_hist);
+    h1 = clamp64(h1, p.n_hist);
+    const int64_t behind = h0 + prompt;
+    each_id(p.hist_ids, h0, h1, v0, n, [&](uint32_t at, int64_t i) {
+      if (i < behind) atomicOr(&count[at], 0x80000000u);
+      else atomicAdd(&count[at], 1u);
+    });
   }
-  int64_t bias0 = 0;
   if (BIAS) {
-    bias0 = clamp64(p.bias_start[row], p.n_bias);
-    const int64_t b = clamp64(p.bias_start[row + 1], p.n_bias);
-    for (int64_t i = bias0 + tid; i < b; i += kLanes) {
-      const uint32_t id = (uint32_t)(p.bias_ids[i] - v0);
-      if (id < (uint32_t)n) atomicMax(&place[id], (uint32_t)(i - bias0) + 1u);
+    b0 = clamp64(b0, p.n_bias);
+    b1 = clamp64(b1, p.n_bias);
+    // the first kLanes entries, most often all of them, stay with their lanes
+    const int64_t i = b0 + tid;
+    uint32_t at = ~0u, value = 0;
+    if (i < b1) {
+      at = (uint32_t)p.bias_ids[i] - (uint32_t)v0;
+      value = __builtin_bit_cast(uint32_t, p.bias_values[i]);
+      if (at < (uint32_t)n) atomicMax(&place[at], (uint32_t)tid + 1u);
+    }
+    each_id(p.bias_ids, b0 + kLanes, b1, v0, n, [&](uint32_t v, int64_t k) { atomicMax(&place[v], (uint32_t)(k - b0) + 1u); });
+    __syncthreads();
+    // who won is known to everybody before the first place is overwritten
+    bool won = at < (uint32_t)n && place[at] == (uint32_t)tid + 1u;
+    if (b1 - b0 <= kLanes) {
+      __syncthreads();
+      if (won) place[at] = value;
+    } else {
+      // a long list: values are looked up from the places, entry by entry
+      uint32_t w[kSteps][kPer];
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) w[s][e] = place[(s * kLanes + tid) * kPer + e];
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+          if (w[s][e]) w[s][e] = __builtin_bit_cast(uint32_t, p.bias_values[b0 + w[s][e] - 1]);
+          place[(s * kLanes + tid) * kPer + e] = w[s][e];
+        }
     }
   }
   if (HIST || BIAS) __syncthreads();
-  const uint32_t* mask = nullptr;
-  if (p.masks) {
-    const int m = p.mask_row ? p.mask_row[row] : row;
-    if ((uint32_t)m < (uint32_t)p.n_masks) mask = p.masks + m * p.mask_stride + (v0 >> 5);
-  }
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
     const int at = (s * kLanes + tid) * kPer;
     if (at >= n) break;
-    const uint32_t allowed = mask ? mask[at >> 5] >> (at & 31) : ~0u;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
       float y = l[s][e];
@@ -116,11 +176,8 @@ __global__ void __launch_bounds__(kLanes) logits_kernel(LogitsParams p) {
         if (w) y = y > 0.0f ? y / rep : y * rep;
         if (c) y = y - freq * (float)c - pres;
       }
-      if (BIAS) {
-        const uint32_t w = place[at + e];
-        if (w) y += p.bias_values[bias0 + w - 1];
-      }
-      l[s][e] = allowed >> e & 1u ? y : -__builtin_inff();
+      if (BIAS) y += __builtin_bit_cast(float, place[at + e]);
+      l[s][e] = allowed[s] >> e & 1u ? y : -__builtin_inff();
     }
     if (at + kPer <= n) {
       Four<TO> w;

@@ -47,54 +47,75 @@ __device__ __forceinline__ uint16_t from_f(float f) { return __builtin_bit_cast(
 // 16-byte chunk of one head; a rotated chunk finds its partners in LDS, where
 // the pass's heads are staged, so any even `rot` and both pairings go the same
 // way and q_out may be q itself (all of a pass is read before it is written).
-// Bound by memory; the sines of a token are computed once per workgroup.
+// Bound by memory, one token by the round trips to it: the rows do not wait
+// for the token's sequence, and of up to 64 sequences every lane reads one's
+// lengths, so the page is the second round trip and the stores follow it. The
+// sines of a token are computed once per workgroup, meanwhile.
 template <class T>
 __global__ void __launch_bounds__(kLanes) rope_kernel(RopeParams p) {
   __shared__ float cs[kMaxPairs], sn[kMaxPairs];
-  __shared__ __attribute__((aligned(16))) uint16_t stage[kLanes * 8];
+  __shared__ __attribute__((aligned(16))) uint16_t stage[2][kLanes * 8];
   const int tok = blockIdx.x, tid = threadIdx.x;
+  const int mine = tid / p.chunks, chunk = tid - mine * p.chunks, first = chunk * 8;
+  const int heads = p.nq + 2 * p.nkv, head0 = blockIdx.y * p.passes * p.per_pass + mine;
+  const auto fetch = [&](int h) {
+    dword4 x = {0, 0, 0, 0};
+    if (mine < p.per_pass && h < heads) {
+      const bool is_q = h < p.nq, is_k = h < p.nq + p.nkv;
+      const RowsView& src = is_q ? p.q : is_k ? p.k : p.v;
+      x = *(const dword4*)(src.p + tok * src.token + (is_q ? h : is_k ? h - p.nq : h - p.nq - p.nkv) * src.head + first);
+    }
+    return x;
+  };
+  dword4 next = fetch(head0);
+  const int pairs = p.rot / 2;
+  const double turns = tid < pairs ? p.turns[tid] : 0.0;
 
   int pos = 0, slot = -1, page = -1;
-  if (p.nkv > 0 || !p.positions) {
-    const SeqView& q = p.seq;
-    const int s = sgemv_dev::wave_upper(q.count, tok, [&](int i) { return (int64_t)q.start(i); });
-    const int a = q.start(s), b = q.start(s + 1);
-    if (tok < a || tok >= b) return;                       // behind the last sequence
-    slot = q.ctx(s) - (b - tok);
-    if (slot >= 0 && p.nkv > 0) page = q.pages[s * q.pages_stride + (slot >> q.page_shift)];
-    pos = slot;
-  }
   if (p.positions) pos = p.positions[tok];
-  const bool store = slot >= 0 && p.seq.page_ok(page);
-
-  const int pairs = p.rot / 2;
+  if (p.nkv > 0) {
+    const SeqView& q = p.seq;
+    int s, a, b, ctx;
+    if (q.count <= 64) {
+      const int lane = tid & 63, i = lane < q.count ? lane : q.count - 1;
+      const int from = q.start(i), to = q.start(i + 1), all = q.ctx(i);
+      const int holds = __popcll(__ballot(lane < q.count && from <= tok));
+      s = holds < 1 ? 0 : holds - 1;
+      a = __builtin_amdgcn_readlane(from, s);
+      b = __builtin_amdgcn_readlane(to, s);
+      ctx = __builtin_amdgcn_readlane(all, s);
+    } else {
+      s = sgemv_dev::wave_upper(q.count, tok, [&](int i) { return q.start(i); });
+      a = q.start(s);
+      b = q.start(s + 1);
+      ctx = q.ctx(s);
+    }
+    if (tok < a || tok >= b) return;                       // of no sequence
+    slot = ctx - (b - tok);
+    if (slot >= 0) page = q.pages[s * q.pages_stride + (slot >> q.page_shift)];
+    if (!p.positions) pos = slot;
+  }
   if (tid < pairs) {
-    const double rev = (double)pos * p.turns[tid];
+    const double rev = (double)pos * turns;
     const float frac = (float)(rev - rint(rev));
     float s, c;
     sincospif(2.0f * frac, &s, &c);
     cs[tid] = c * p.magnitude;
     sn[tid] = s * p.magnitude;
   }
-
-  const int mine = tid / p.chunks, chunk = tid - mine * p.chunks;
-  const int heads = p.nq + 2 * p.nkv, head0 = blockIdx.y * p.passes * p.per_pass;
-  const int64_t in_page = (slot & ((1 << p.seq.page_shift) - 1));
+  const bool store = slot >= 0 && p.seq.page_ok(page);
+  const int64_t in_page = slot & ((1 << p.seq.page_shift) - 1);
   for (int pass = 0; pass < p.passes; ++pass) {
-    const int h = head0 + pass * p.per_pass + mine;
-    const bool live = mine < p.per_pass && h < heads;
+    const int h = head0 + pass * p.per_pass;
+    dword4 x = next;
+    uint16_t* part = stage[pass & 1];
+    *(dword4*)(part + tid * 8) = x;
+    if (pass + 1 < p.passes) next = fetch(h + p.per_pass);
+    __syncthreads();                                       // two parts: nobody still reads the one written next
     const bool is_q = h < p.nq, is_k = !is_q && h < p.nq + p.nkv;
-    const int hh = is_q ? h : is_k ? h - p.nq : h - p.nq - p.nkv;
-    const RowsView& src = is_q ? p.q : is_k ? p.k : p.v;
-    dword4 x = {0, 0, 0, 0};
-    if (live) x = *(const dword4*)(src.p + tok * src.token + hh * src.head + chunk * 8);
-    if (pass) __syncthreads();                             // the last pass's partners have been read
-    *(dword4*)(stage + tid * 8) = x;
-    __syncthreads();
-    if (!live || (!is_q && !store)) continue;
-    const int first = chunk * 8;
+    if (mine >= p.per_pass || h >= heads || (!is_q && !store)) continue;
     if ((is_q || is_k) && first < p.rot) {
-      const uint16_t* head = stage + (tid - chunk) * 8;
+      const uint16_t* head = part + (tid - chunk) * 8;
       uint16_t y[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -110,6 +131,7 @@ __global__ void __launch_bounds__(kLanes) rope_kernel(RopeParams p) {
       }
       x = *(const dword4*)y;
     }
+    const int hh = is_q ? h : is_k ? h - p.nq : h - p.nq - p.nkv;
     uint16_t* dst = is_q ? p.q_out.p + tok * p.q_out.token + hh * p.q_out.head
                          : is_k ? p.kc.p + page * p.k_page + in_page * p.kc.token + hh * p.kc.head
                                 : p.vc.p + page * p.v_page + in_page * p.vc.token + hh * p.vc.head;

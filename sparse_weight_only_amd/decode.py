@@ -104,14 +104,21 @@ def _ref(x):
     return None if x is None else ctypes.byref(x)
 
 
-_types = None
+# torch and what is looked up in it on every call, set by _init (the library's
+# host side is used without torch)
+torch = _types = _raw_stream = None
+
+
+def _init():
+    global torch, _types, _raw_stream
+    import torch as t
+    _types = {t.float16: F16, t.bfloat16: BF16, t.float32: F32}
+    # the raw current stream without building a Stream object, which costs more than the rest of a call's checks
+    _raw_stream = getattr(t._C, "_cuda_getCurrentRawStream", None) or (lambda i: t.cuda.current_stream(i).cuda_stream)
+    torch = t
 
 
 def _type(dtype) -> int:
-    global _types
-    if _types is None:
-        import torch
-        _types = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
     try:
         return _types[dtype]
     except KeyError:
@@ -119,10 +126,12 @@ def _type(dtype) -> int:
 
 
 def _rows(x, what: str) -> Rows:
-    if x.dim() != 3 or (x.stride(2) != 1 and x.shape[2] > 1):
-        raise ValueError(f"{what} must be [tokens, heads, head_dim] with contiguous columns")
-    st, sh, _ = x.stride()
+    if x.dim() != 3:
+        raise ValueError(f"{what} must be [tokens, heads, head_dim]")
+    st, sh, sd = x.stride()
     t, h, d = x.shape
+    if sd != 1 and d > 1:
+        raise ValueError(f"{what} must have contiguous columns")
     return Rows(x.data_ptr(), st, sh, t, h, d, _type(x.dtype))
 
 
@@ -133,8 +142,7 @@ def _on(device, **tensors) -> None:
 
 
 def _ints(x, what: str, shape=None) -> None:
-    import torch
-    if x.dtype != torch.int32 or not x.is_contiguous() or (shape is not None and tuple(x.shape) != shape):
+    if x.dtype != torch.int32 or not x.is_contiguous() or (shape is not None and x.shape != shape):
         raise ValueError(f"{what} must be a contiguous int32 tensor" + (f" of shape {list(shape)}" if shape is not None else ""))
 
 
@@ -145,18 +153,17 @@ class _Launch:
     __slots__ = ("device", "stream", "ctx")
 
     def __init__(self, device, stream):
+        if device.type != "cuda":
+            raise ValueError(f"tensors are on {device}, not on a GPU")
         self.device, self.stream, self.ctx = device, stream, None
 
     def __enter__(self) -> int:
-        import torch
-        if self.device.type != "cuda":
-            raise ValueError(f"tensors are on {self.device}, not on a GPU")
-        s = self.stream
+        i, s = self.device.index, self.stream
         if s is None:
-            if torch.cuda.current_device() != self.device.index:
-                self.ctx = torch.cuda.device(self.device)
+            if torch.cuda.current_device() != i:
+                self.ctx = torch.cuda.device(i)
                 self.ctx.__enter__()
-            return torch.cuda.current_stream(self.device).cuda_stream
+            return _raw_stream(i)
         if s.device != self.device:
             raise ValueError(f"the stream is on {s.device}, the tensors on {self.device}")
         self.ctx = torch.cuda.stream(s)
@@ -178,13 +185,12 @@ class Rope:
 
     def __init__(self, rot_dim: int, base: float = 10000.0, interleaved: bool = False, factor: float = 1.0,
                  context: float = 0.0, low: float = 1.0, high: float = 32.0, magnitude: float = 1.0, device="cuda"):
-        import torch
+        _init()
         self.turns = torch.from_numpy(rope_table(rot_dim, base, factor, context, low, high)).to(device)
         self.args = RopeArgs(self.turns.data_ptr(), rot_dim, int(bool(interleaved)), magnitude)
 
     def apply(self, x, positions, out=None, stream=None):
         """x [tokens, heads, head_dim] turned at ``positions`` (int32 [tokens]) into ``out`` (a new tensor; x itself is fine)."""
-        import torch
         _ints(positions, "positions", (x.shape[0],))
         _on(self.turns.device, x=x, positions=positions, out=out)
         xr = _rows(x, "x")
@@ -205,7 +211,7 @@ class Sequences:
     """
 
     def __init__(self, new_start, ctx_len, pages):
-        import torch
+        _init()
         count = ctx_len.shape[0]
         _ints(ctx_len, "ctx_len", (count,))
         _ints(new_start, "new_start", (count + 1,))
@@ -223,7 +229,7 @@ class PagedCache:
     heads, head_dim], FP16 or BF16."""
 
     def __init__(self, pages: int, page_size: int, heads: int, head_dim: int, dtype=None, device="cuda"):
-        import torch
+        _init()
         shape = (pages, page_size, heads, head_dim)
         self._set(*(torch.zeros(shape, dtype=dtype or torch.float16, device=device) for _ in range(2)))
 
@@ -231,6 +237,7 @@ class PagedCache:
     def from_tensors(cls, k, v) -> "PagedCache":
         """A cache over tensors of the caller's, of any strides with
         contiguous columns (a head-major cache is passed transposed)."""
+        _init()
         self = cls.__new__(cls)
         self._set(k, v)
         return self
@@ -250,7 +257,6 @@ class PagedCache:
         head_dim], in their slots; q [tokens, query heads, head_dim] turned
         into ``q_out`` (a new tensor; q itself is fine), which is returned.
         ``positions`` (int32 [tokens]): instead of the tokens' slots."""
-        import torch
         if rope is None and (q is not None or positions is not None):
             raise ValueError("q and positions need a rope")
         if q is None and q_out is not None:
@@ -281,7 +287,6 @@ class PagedCache:
         more, not shared with calls that may run at the same time; made if
         not given. Rows of no sequence stay as they are in a given ``out``
         and are undefined in a new one."""
-        import torch
         words = 0
         if tree is not None:
             _ints(tree, "tree")
@@ -316,54 +321,58 @@ def adjust_logits(x, out=None, history=None, history_start=None, prompt_len=None
     bias_ids, bias_values, bias_start: a ragged list as the history; masks
     (int32 [n, (vocab + 31) / 32]): bit v of a mask set where token v is
     allowed; mask_row (int32 [rows]): each row's mask, -1 for none."""
-    import torch
-    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
-        raise ValueError("x must be [rows, vocab] with contiguous rows")
-    rows, vocab = x.shape
-    if out is not None and (out.shape != x.shape or (vocab > 1 and out.stride(1) != 1)):
-        raise ValueError("out must have the shape of x, and contiguous rows")
+    if torch is None:
+        _init()
     dev = x.device
-    if (history is None) != (history_start is None):
-        raise ValueError("history and history_start belong together")
-    if (bias_ids is None) != (bias_start is None) or (bias_ids is None) != (bias_values is None):
-        raise ValueError("bias_ids, bias_values and bias_start belong together")
-    g = Logits(x=x.data_ptr(), x_stride=x.stride(0), rows=rows, vocab=vocab, dtype=_type(x.dtype))
-    if history is not None:
-        _on(dev, history=history, history_start=history_start)
-        _ints(history, "history", (history.numel(),))
-        _ints(history_start, "history_start", (rows + 1,))
-        g.hist_ids, g.hist_start, g.n_hist = history.data_ptr(), history_start.data_ptr(), history.numel()
+    rows, vocab = x.shape if x.dim() == 2 else (-1, -1)
+    sx, cx = x.stride() if rows >= 0 else (0, 0)
+    if rows < 0 or (cx != 1 and vocab > 1):
+        raise ValueError("x must be [rows, vocab] with contiguous rows")
+    if out is not None and (out.shape != x.shape or (out.stride(1) != 1 and vocab > 1) or out.device != dev):
+        raise ValueError(f"out must have the shape of x, and contiguous rows, on {dev}")
+
+    def at(t, what, n, dtype):
+        if t.dtype != dtype or t.shape != n or not t.is_contiguous() or t.device != dev:
+            raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {list(n)} on {dev}")
+        return t.data_ptr()
+
+    i32, f32 = torch.int32, torch.float32
+    one, ends = (rows,), (rows + 1,)
+    g = Logits(x.data_ptr(), 0, sx, 0)
+    g.rows, g.vocab, g.dtype = rows, vocab, _type(x.dtype)
+    if history is not None or history_start is not None:
+        if history is None or history_start is None:
+            raise ValueError("history and history_start belong together")
+        n = history.numel()
+        g.hist_ids, g.hist_start, g.n_hist = at(history, "history", (n,), i32), at(history_start, "history_start", ends, i32), n
     if prompt_len is not None:
-        _on(dev, prompt_len=prompt_len)
-        _ints(prompt_len, "prompt_len", (rows,))
-        g.prompt_len = prompt_len.data_ptr()
-    for what, t in (("repetition", repetition), ("frequency", frequency), ("presence", presence)):
-        if t is not None:
-            if t.dtype != torch.float32 or t.shape != (rows,) or not t.is_contiguous() or t.device != dev:
-                raise ValueError(f"{what} must be a contiguous float32 tensor of shape [{rows}] on {dev}")
-            setattr(g, what, t.data_ptr())
-    if bias_ids is not None:
-        _on(dev, bias_ids=bias_ids, bias_start=bias_start, bias_values=bias_values)
-        _ints(bias_ids, "bias_ids", (bias_ids.numel(),))
-        _ints(bias_start, "bias_start", (rows + 1,))
-        if bias_values.dtype != torch.float32 or bias_values.shape != bias_ids.shape or not bias_values.is_contiguous():
-            raise ValueError("bias_values must be a contiguous float32 tensor, one for each of bias_ids")
-        g.bias_ids, g.bias_start, g.bias_values, g.n_bias = (bias_ids.data_ptr(), bias_start.data_ptr(), bias_values.data_ptr(),
-                                                             bias_ids.numel())
+        g.prompt_len = at(prompt_len, "prompt_len", one, i32)
+    if repetition is not None:
+        g.repetition = at(repetition, "repetition", one, f32)
+    if frequency is not None:
+        g.frequency = at(frequency, "frequency", one, f32)
+    if presence is not None:
+        g.presence = at(presence, "presence", one, f32)
+    if bias_ids is not None or bias_values is not None or bias_start is not None:
+        if bias_ids is None or bias_values is None or bias_start is None:
+            raise ValueError("bias_ids, bias_values and bias_start belong together")
+        n = bias_ids.numel()
+        g.bias_ids, g.bias_values, g.n_bias = at(bias_ids, "bias_ids", (n,), i32), at(bias_values, "bias_values", (n,), f32), n
+        g.bias_start = at(bias_start, "bias_start", ends, i32)
     if masks is not None:
-        _on(dev, masks=masks, mask_row=mask_row)
-        if masks.dtype != torch.int32 or masks.dim() != 2 or masks.shape[1] != (vocab + 31) // 32 or (masks.shape[1] > 1 and masks.stride(1) != 1):
-            raise ValueError(f"masks must be an int32 tensor of shape [n, {(vocab + 31) // 32}] with contiguous rows")
+        words = (vocab + 31) // 32
+        if masks.dtype != i32 or masks.dim() != 2 or masks.shape[1] != words or (words > 1 and masks.stride(1) != 1) or masks.device != dev:
+            raise ValueError(f"masks must be an int32 tensor of shape [n, {words}] with contiguous rows on {dev}")
         g.masks, g.mask_stride, g.n_masks = masks.data_ptr(), masks.stride(0), masks.shape[0]
         if mask_row is not None:
-            _ints(mask_row, "mask_row", (rows,))
-            g.mask_row = mask_row.data_ptr()
+            g.mask_row = at(mask_row, "mask_row", one, i32)
     elif mask_row is not None:
         raise ValueError("mask_row needs masks")
-    _on(dev, out=out)
     with _Launch(dev, stream) as s:
         if out is None:
-            out = torch.empty(x.shape, dtype=torch.float32, device=dev)
+            out = torch.empty(x.shape, dtype=f32, device=dev)
         g.out, g.out_stride, g.out_dtype = out.data_ptr(), out.stride(0), _type(out.dtype)
-        _check(lib().sgemv_adjust_logits(_ref(g), s), "sgemv_adjust_logits")
+        code = lib().sgemv_adjust_logits(ctypes.byref(g), s)
+    if code:
+        _check(code, "sgemv_adjust_logits")
     return out

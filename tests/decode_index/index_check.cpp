@@ -68,17 +68,17 @@ int main() {
     p.tree_words = words;
     p.group = group;
     p.splits = pick(1, 5);
-    for (const auto& mb : {std::pair<int, int>{16, 32}, {128, 64}, {256, 64}}) {
+    for (const auto& mb : {std::pair<int, int>{16, 32}, {128, 64}, {256, 64}, {256, 32}}) {
       const int m = mb.first, block = mb.second;
       const int slots = (int)((int64_t)tokens * group / m + count);
       std::map<std::pair<int, int>, int> rows_seen;   // (token, head of the group) -> tiles
       for (int slot = 0; slot < slots; ++slot) {
-        const int s = upper(count, slot, [&](int i) { return slot_base(p, i, m); });
+        const int s = upper(count, slot, [&](int i) { return slot_base(p, i, p.seq.start(i), m); });
         REQUIRE(s >= 0 && s < count);
         int at_key = 0;
         for (int split = 0; split < p.splits; ++split) {
           Tile t;
-          if (!make_tile(p, m, block, s, slot, split, t)) break;
+          if (!make_tile(p, m, block, s, p.seq.start(s), p.seq.start(s + 1), p.seq.ctx(s), slot, split, t)) break;
           REQUIRE(t.row0 >= 0 && t.row0 < t.rows && t.first >= 0 && t.first + t.n <= tokens);
           REQUIRE(t.key0 <= t.key1 && t.key1 <= t.end && t.end <= per << shift);
           REQUIRE(split == 0 ? t.key0 == 0 : t.key0 == at_key);
@@ -86,7 +86,7 @@ int main() {
           if (split == p.splits - 1) REQUIRE(t.key1 == t.end);
           // the join finds the same parts from split 0 alone
           Tile j = t;
-          tile_keys(p, m, block, 0, j);
+          tile_keys(p, m, block, p.seq.ctx(s), 0, j);
           const int len = j.key1, parts = len > 0 ? (j.end + len - 1) / len : 0;
           REQUIRE(parts <= p.splits && (t.key0 < t.key1) == (split < parts));
           int sum = 0;
