@@ -59,17 +59,35 @@ __device__ __forceinline__ void each_id(const int32_t* ids, int64_t a, int64_t b
   }
 }
 
+constexpr int kShort = 4;                            // bias entries that a lane holds
+constexpr int kListed = 256;                         // bias entries of a part that the lanes can go through
+
+// The first two steps for one logit: w is its word of counts.
+__device__ __forceinline__ float penalised(float y, uint32_t w, float rep, float freq, float pres) {
+  const uint32_t c = w & 0x7fffffffu;
+  if (w) y = y > 0.0f ? y / rep : y * rep;
+  if (c) y = y - freq * (float)c - pres;
+  return y;
+}
+
 // Workgroup (c, b): entries c kPart .. of row b. The counts of its entries are
 // kept in LDS: every lane walks the history and counts the ids that fall into
-// the part (whole numbers, so the order of the atomics does not matter). Of a
-// bias id given twice the later place wins, by an atomic maximum of the places;
-// then the winners put their values where the places were.
+// the part (whole numbers, so the order of the atomics does not matter).
+// A bias list has few entries in a part (300 in 32 parts, say). The lanes that
+// hold them work out those logits themselves and write them once the part has
+// been written: of an id given twice the entry with the later place does, which
+// each lane knows from the part's entries in LDS (their order there does not
+// matter). A longer list, or more entries in one part, goes through a table of
+// places instead, by an atomic maximum, in the words of the counts (a table of
+// its own for every list cost a third of the waves of a compute unit: 93 us
+// for 256 x 128003 logits with 300 entries a row, 63 without any).
 // Bound by memory for a batch, by its round trips for one row: everything that
 // does not wait for something else is asked for at the start.
 template <class TI, class TO, bool HIST, bool BIAS>
 __global__ void __launch_bounds__(kLanes) logits_kernel(LogitsParams p) {
-  __shared__ uint32_t count[HIST ? kPart : 1];       // bit 31: in the prompt; below: how often behind it
-  __shared__ uint32_t place[BIAS ? kPart : 1];       // place in the row's bias list + 1, then the bias
+  __shared__ uint32_t count[HIST || BIAS ? kPart : 1];   // bit 31: in the prompt; below: how often behind it
+  __shared__ uint32_t listed[BIAS ? kListed : 1];        // bias entries of the part: entry << 16 | place
+  __shared__ int n_listed;
   const int tid = threadIdx.x, row = blockIdx.y;
   const int v0 = blockIdx.x * kPart;
   const int n = p.vocab - v0 < kPart ? p.vocab - v0 : kPart;
@@ -79,6 +97,10 @@ __global__ void __launch_bounds__(kLanes) logits_kernel(LogitsParams p) {
   int64_t h0 = 0, h1 = 0, b0 = 0, b1 = 0;
   int prompt = 0, m = -1;
   float rep = 1.0f, freq = 0.0f, pres = 0.0f;
+  if (BIAS) {
+    b0 = p.bias_start[row];
+    b1 = p.bias_start[row + 1];
+  }
   if (HIST) {
     h0 = p.hist_start[row];
     h1 = p.hist_start[row + 1];
@@ -86,10 +108,6 @@ __global__ void __launch_bounds__(kLanes) logits_kernel(LogitsParams p) {
     if (p.repetition) rep = p.repetition[row];
     if (p.frequency) freq = p.frequency[row];
     if (p.presence) pres = p.presence[row];
-  }
-  if (BIAS) {
-    b0 = p.bias_start[row];
-    b1 = p.bias_start[row + 1];
   }
   if (p.masks) m = p.mask_row ? p.mask_row[row] : row;
   float l[kSteps][kPer];
@@ -105,20 +123,44 @@ __global__ void __launch_bounds__(kLanes) logits_kernel(LogitsParams p) {
       for (int e = 0; e < kPer; ++e) l[s][e] = at + e < n ? (float)x[at + e] : 0.0f;
     }
   }
-  uint32_t allowed[kSteps];
   const bool masked = (uint32_t)m < (uint32_t)p.n_masks;
+  const uint32_t* mask = masked ? p.masks + m * p.mask_stride + (v0 >> 5) : nullptr;
+  uint32_t allowed[kSteps];
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
     const int at = (s * kLanes + tid) * kPer;
-    allowed[s] = masked && at < n ? p.masks[m * p.mask_stride + ((v0 + at) >> 5)] >> (at & 31) : ~0u;
+    allowed[s] = masked && at < n ? mask[at >> 5] >> (at & 31) : ~0u;
   }
   if (HIST || BIAS) {
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      if (HIST) *(sgemv_dev::dword4*)&count[(s * kLanes + tid) * kPer] = sgemv_dev::dword4{0, 0, 0, 0};
-      if (BIAS) *(sgemv_dev::dword4*)&place[(s * kLanes + tid) * kPer] = sgemv_dev::dword4{0, 0, 0, 0};
-    }
+    for (int s = 0; s < kSteps; ++s) *(sgemv_dev::dword4*)&count[(s * kLanes + tid) * kPer] = sgemv_dev::dword4{0, 0, 0, 0};
+    if (BIAS && tid == 0) n_listed = 0;
     __syncthreads();
+  }
+  uint32_t mine[kShort];                                 // entries of the part that this lane holds; n or more: none
+  float value[kShort], logit[kShort];
+  uint32_t bit[kShort];
+  bool table = false;
+  if (BIAS) {
+    b0 = clamp64(b0, p.n_bias);
+    b1 = clamp64(b1, p.n_bias);
+    table = b1 - b0 > kShort * kLanes;
+#pragma unroll
+    for (int k = 0; k < kShort; ++k) {
+      const int64_t i = b0 + k * kLanes + tid;
+      mine[k] = !table && i < b1 ? (uint32_t)p.bias_ids[i] - (uint32_t)v0 : ~0u;
+    }
+#pragma unroll
+    for (int k = 0; k < kShort; ++k) {
+      bit[k] = 1u;
+      if (mine[k] < (uint32_t)n) {
+        const int to = atomicAdd(&n_listed, 1);
+        if (to < kListed) listed[to] = mine[k] << 16 | (uint32_t)(k * kLanes + tid);
+        value[k] = p.bias_values[b0 + k * kLanes + tid];
+        logit[k] = (float)x[mine[k]];
+        if (masked) bit[k] = mask[mine[k] >> 5] >> (mine[k] & 31) & 1u;
+      }
+    }
   }
   if (HIST) {
     h0 = clamp64(h0, p.n_hist);
@@ -129,56 +171,37 @@ __global__ void __launch_bounds__(kLanes) logits_kernel(LogitsParams p) {
       else atomicAdd(&count[at], 1u);
     });
   }
-  if (BIAS) {
-    b0 = clamp64(b0, p.n_bias);
-    b1 = clamp64(b1, p.n_bias);
-    // the first kLanes entries, most often all of them, stay with their lanes
-    const int64_t i = b0 + tid;
-    uint32_t at = ~0u, value = 0;
-    if (i < b1) {
-      at = (uint32_t)p.bias_ids[i] - (uint32_t)v0;
-      value = __builtin_bit_cast(uint32_t, p.bias_values[i]);
-      if (at < (uint32_t)n) atomicMax(&place[at], (uint32_t)tid + 1u);
-    }
-    each_id(p.bias_ids, b0 + kLanes, b1, v0, n, [&](uint32_t v, int64_t k) { atomicMax(&place[v], (uint32_t)(k - b0) + 1u); });
-    __syncthreads();
-    // who won is known to everybody before the first place is overwritten
-    bool won = at < (uint32_t)n && place[at] == (uint32_t)tid + 1u;
-    if (b1 - b0 <= kLanes) {
-      __syncthreads();
-      if (won) place[at] = value;
-    } else {
-      // a long list: values are looked up from the places, entry by entry
-      uint32_t w[kSteps][kPer];
+  if (HIST || BIAS) __syncthreads();
+  if (HIST) {
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s)
+    for (int s = 0; s < kSteps; ++s) {
+      const sgemv_dev::dword4 w = *(const sgemv_dev::dword4*)&count[(s * kLanes + tid) * kPer];
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) w[s][e] = place[(s * kLanes + tid) * kPer + e];
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-          if (w[s][e]) w[s][e] = __builtin_bit_cast(uint32_t, p.bias_values[b0 + w[s][e] - 1]);
-          place[(s * kLanes + tid) * kPer + e] = w[s][e];
-        }
+      for (int e = 0; e < kPer; ++e) l[s][e] = penalised(l[s][e], w[e], rep, freq, pres);
     }
   }
-  if (HIST || BIAS) __syncthreads();
+  if (BIAS && (table || n_listed > kListed)) {
+    table = true;
+    __syncthreads();                                     // all counts have been read
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) *(sgemv_dev::dword4*)&count[(s * kLanes + tid) * kPer] = sgemv_dev::dword4{0, 0, 0, 0};
+    __syncthreads();
+    each_id(p.bias_ids, b0, b1, v0, n, [&](uint32_t v, int64_t i) { atomicMax(&count[v], (uint32_t)(i - b0) + 1u); });
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const sgemv_dev::dword4 w = *(const sgemv_dev::dword4*)&count[(s * kLanes + tid) * kPer];
+#pragma unroll
+      for (int e = 0; e < kPer; ++e)
+        if (w[e]) l[s][e] += p.bias_values[b0 + w[e] - 1];
+    }
+  }
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
     const int at = (s * kLanes + tid) * kPer;
     if (at >= n) break;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      float y = l[s][e];
-      if (HIST) {
-        const uint32_t w = count[at + e], c = w & 0x7fffffffu;
-        if (w) y = y > 0.0f ? y / rep : y * rep;
-        if (c) y = y - freq * (float)c - pres;
-      }
-      if (BIAS) y += __builtin_bit_cast(float, place[at + e]);
-      l[s][e] = allowed[s] >> e & 1u ? y : -__builtin_inff();
-    }
+    for (int e = 0; e < kPer; ++e) l[s][e] = allowed[s] >> e & 1u ? l[s][e] : -__builtin_inff();
     if (at + kPer <= n) {
       Four<TO> w;
 #pragma unroll
@@ -188,6 +211,22 @@ __global__ void __launch_bounds__(kLanes) logits_kernel(LogitsParams p) {
 #pragma unroll
       for (int e = 0; e < kPer; ++e)
         if (at + e < n) out[at + e] = (TO)l[s][e];
+    }
+  }
+  if (BIAS && !table && n_listed > 0) {
+    // the part has been written, by every wave, before an entry is written again
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kShort; ++k) {
+      if (mine[k] >= (uint32_t)n) continue;
+      bool last = true;
+      const uint32_t me = mine[k] << 16 | (uint32_t)(k * kLanes + tid);
+      for (int i = 0; i < n_listed; ++i) last &= listed[i] >> 16 != mine[k] || listed[i] <= me;
+      if (!last) continue;
+      float y = logit[k];
+      if (HIST) y = penalised(y, count[mine[k]], rep, freq, pres);
+      out[mine[k]] = (TO)(bit[k] ? y + value[k] : -__builtin_inff());
     }
   }
 }

@@ -13,7 +13,6 @@ stream that it runs on.
 from __future__ import annotations
 
 import ctypes
-import math
 
 import numpy as np
 
@@ -100,8 +99,11 @@ def attend(cache: Cache, seqs: Seqs, q: Rows, out: Rows, scale: float, tree_dev:
                               stream), "sgemv_attend")
 
 
+_byref = ctypes.byref
+
+
 def _ref(x):
-    return None if x is None else ctypes.byref(x)
+    return None if x is None else _byref(x)
 
 
 # torch and what is looked up in it on every call, set by _init (the library's
@@ -146,33 +148,29 @@ def _ints(x, what: str, shape=None) -> None:
         raise ValueError(f"{what} must be a contiguous int32 tensor" + (f" of shape {list(shape)}" if shape is not None else ""))
 
 
-class _Launch:
-    """The device and stream of a call: ``with _Launch(device, stream) as s``
-    makes both current (kernels are launched on the current device, and
-    tensors made inside belong to the stream) and gives the raw stream."""
-    __slots__ = ("device", "stream", "ctx")
+def _enter(device, stream):
+    """Makes a call's device and stream current (kernels are launched on the
+    current device, and tensors made meanwhile belong to the stream): the raw
+    stream, and what to leave again, None where both were current already."""
+    if device.type != "cuda":
+        raise ValueError(f"tensors are on {device}, not on a GPU")
+    i = device.index
+    if stream is None:
+        if torch.cuda.current_device() == i:
+            return _raw_stream(i), None
+        ctx = torch.cuda.device(i)
+        ctx.__enter__()
+        return _raw_stream(i), ctx
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    ctx = torch.cuda.stream(stream)
+    ctx.__enter__()
+    return stream.cuda_stream, ctx
 
-    def __init__(self, device, stream):
-        if device.type != "cuda":
-            raise ValueError(f"tensors are on {device}, not on a GPU")
-        self.device, self.stream, self.ctx = device, stream, None
 
-    def __enter__(self) -> int:
-        i, s = self.device.index, self.stream
-        if s is None:
-            if torch.cuda.current_device() != i:
-                self.ctx = torch.cuda.device(i)
-                self.ctx.__enter__()
-            return _raw_stream(i)
-        if s.device != self.device:
-            raise ValueError(f"the stream is on {s.device}, the tensors on {self.device}")
-        self.ctx = torch.cuda.stream(s)
-        self.ctx.__enter__()
-        return s.cuda_stream
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _leave(ctx) -> None:
+    if ctx is not None:
+        ctx.__exit__(None, None, None)
 
 
 class Rope:
@@ -194,10 +192,13 @@ class Rope:
         _ints(positions, "positions", (x.shape[0],))
         _on(self.turns.device, x=x, positions=positions, out=out)
         xr = _rows(x, "x")
-        with _Launch(x.device, stream) as s:
+        s, ctx = _enter(x.device, stream)
+        try:
             if out is None:
                 out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
             rope(self.args, positions.data_ptr(), xr, _rows(out, "out"), s)
+        finally:
+            _leave(ctx)
         return out
 
 
@@ -261,15 +262,22 @@ class PagedCache:
             raise ValueError("q and positions need a rope")
         if q is None and q_out is not None:
             raise ValueError("q_out needs q")
+        dev = self.device
         if positions is not None:
             _ints(positions, "positions", (k.shape[0],))
-        _on(self.device, k=k, v=v, q=q, q_out=q_out, positions=positions, seqs=seqs, rope=rope and rope.turns)
-        qr, kr, vr = None if q is None else _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
-        with _Launch(self.device, stream) as s:
+        _on(dev, k=k, v=v, q=q, q_out=q_out, positions=positions, seqs=seqs, rope=rope and rope.turns)
+        qr, kr, vr = None if q is None else _ref(_rows(q, "q")), _rows(k, "k"), _rows(v, "v")
+        s, ctx = _enter(dev, stream)
+        try:
             if q is not None and q_out is None:
                 q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            append(self.args, seqs.args, rope and rope.args, positions.data_ptr() if positions is not None else 0,
-                   qr, None if q is None else _rows(q_out, "q_out"), kr, vr, s)
+            code = lib().sgemv_append(_ref(self.args), _ref(seqs.args), None if rope is None else _ref(rope.args),
+                                      0 if positions is None else positions.data_ptr(), qr,
+                                      None if q is None else _ref(_rows(q_out, "q_out")), _ref(kr), _ref(vr), s)
+        finally:
+            _leave(ctx)
+        if code:
+            _check(code, "sgemv_append")
         return q_out
 
     def plan(self, seqs: Sequences, tokens: int, heads: int, max_ctx: int = 0) -> AttendPlan:
@@ -287,26 +295,36 @@ class PagedCache:
         more, not shared with calls that may run at the same time; made if
         not given. Rows of no sequence stay as they are in a given ``out``
         and are undefined in a new one."""
-        words = 0
+        dev = self.device
+        words = at = 0
         if tree is not None:
             _ints(tree, "tree")
             if tree.dim() != 2 or tree.shape[0] != q.shape[0]:
                 raise ValueError("tree must be [tokens, words]")
-            words = tree.shape[1]
+            words, at = tree.shape[1], tree.data_ptr()
         if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
             raise ValueError("workspace must be a contiguous uint8 tensor")
-        _on(self.device, q=q, seqs=seqs, tree=tree, out=out, workspace=workspace)
+        _on(dev, q=q, seqs=seqs, tree=tree, out=out, workspace=workspace)
         qr = _rows(q, "q")
-        with _Launch(self.device, stream) as s:
+        s, ctx = _enter(dev, stream)
+        try:
             if out is None:
-                out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+                out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            L, c, sq = lib(), _ref(self.args), _ref(seqs.args)
             if workspace is None:
-                need = attend_plan(self.args, seqs.args, qr.tokens, qr.heads, max_ctx).workspace_bytes
-                if need:
-                    workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
-            attend(self.args, seqs.args, qr, _rows(out, "out"), 1.0 / math.sqrt(q.shape[2]) if scale is None else scale,
-                   tree.data_ptr() if tree is not None else 0, words, max_ctx,
-                   workspace.data_ptr() if workspace is not None else 0, workspace.numel() if workspace is not None else 0, s)
+                pl = AttendPlan()
+                code = L.sgemv_attend_plan(c, sq, qr.tokens, qr.heads, max_ctx, _ref(pl))
+                if code:
+                    _check(code, "sgemv_attend_plan")
+                if pl.workspace_bytes:
+                    workspace = torch.empty(pl.workspace_bytes, dtype=torch.uint8, device=dev)
+            scratch, room = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+            code = L.sgemv_attend(c, sq, _ref(qr), _ref(_rows(out, "out")), qr.head_dim ** -0.5 if scale is None else scale,
+                                  at, words, max_ctx, scratch, room, s)
+        finally:
+            _leave(ctx)
+        if code:
+            _check(code, "sgemv_attend")
         return out
 
 
@@ -368,11 +386,14 @@ def adjust_logits(x, out=None, history=None, history_start=None, prompt_len=None
             g.mask_row = at(mask_row, "mask_row", one, i32)
     elif mask_row is not None:
         raise ValueError("mask_row needs masks")
-    with _Launch(dev, stream) as s:
+    s, ctx = _enter(dev, stream)
+    try:
         if out is None:
             out = torch.empty(x.shape, dtype=f32, device=dev)
         g.out, g.out_stride, g.out_dtype = out.data_ptr(), out.stride(0), _type(out.dtype)
         code = lib().sgemv_adjust_logits(ctypes.byref(g), s)
+    finally:
+        _leave(ctx)
     if code:
         _check(code, "sgemv_adjust_logits")
     return out

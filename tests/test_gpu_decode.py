@@ -515,6 +515,27 @@ def test_logits_bias_given_twice():
     assert np.array_equal(host(out)[0], want)
 
 
+@pytest.mark.parametrize("n", [1, 2, 7, 256, 257, 1024, 1025, 3000])
+@pytest.mark.parametrize("spread", [1, 40, 9000])
+def test_logits_bias_lists_of_any_length(n, spread):
+    """Copies in one part or over several, lists that the lanes hold and longer ones, in place too."""
+    say("case bias lists", n, spread)
+    rng = np.random.default_rng(n + spread)
+    ids = [rng.integers(0, spread, k) for k in (n, 0, n)]
+    vals = [rng.integers(-50, 50, k) * 0.25 for k in (n, 0, n)]
+    x = torch.randint(-9, 9, (3, 9001), device="cuda").float()
+    m = rng.random((1, 9001)) < 0.7
+    h = [[3, 3, 5], list(range(50)), []]
+    flat, start = ragged(ids, torch.int32)
+    hist, hist_start = ragged(h, torch.int32)
+    two = torch.full((3,), 2.0, device="cuda")
+    args = dict(bias_ids=flat, bias_start=start, bias_values=ragged(vals, F32)[0], history=hist, history_start=hist_start, repetition=two, frequency=two,
+                masks=bits(m), mask_row=ints([0, 0, -1]))
+    ref = odec.adjust_logits(host(x), h, repetition=[2.0] * 3, frequency=[2.0] * 3, bias=[list(zip(i, v)) for i, v in zip(ids, vals)], masks=[m[0], m[0], None])
+    assert np.array_equal(host(sg.adjust_logits(x, **args)), ref)          # every step is exact in these numbers
+    assert np.array_equal(host(sg.adjust_logits(x, out=x, **args)), ref)
+
+
 def test_logits_special_values():
     """NaN and infinities in masked places are gone, in others they follow the formula; a row may be left with nothing."""
     say("case logits special")
