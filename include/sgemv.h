@@ -536,7 +536,7 @@ typedef struct sgemv_logits {
 /* sgemv_adjust_logits - in this order, in FP32, rounded once:
  *   l <- l > 0 ? l / repetition : l * repetition  for ids in the history
  *   l <- l - frequency n - presence               for ids n > 0 times behind the prompt
- *   l <- l + bias                                 (an id given twice: its last place holds)
+ *   l <- l + bias                                 (an id given twice: its first place holds)
  *   l <- -inf                                     for ids the row's mask does not allow
  * A grammar or a prefix tree gives its states' allowed tokens as masks. A row
  * may be left with none: all -inf. Enqueues one kernel and returns without

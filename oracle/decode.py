@@ -116,8 +116,11 @@ def adjust_logits(x, history=None, prompt_len=None, repetition=None, frequency=N
                 y[b, v] -= (0.0 if frequency is None else float(frequency[b])) * n
                 y[b, v] -= 0.0 if presence is None else float(presence[b])
         if bias is not None:
-            for v, a in {int(i): float(a) for i, a in bias[b] if 0 <= i < vocab}.items():
-                y[b, v] += a
+            done = set()                     # an id given twice: the first one holds
+            for v, a in bias[b]:
+                if 0 <= v < vocab and int(v) not in done:
+                    done.add(int(v))
+                    y[b, int(v)] += float(a)
         if masks is not None and masks[b] is not None:
             y[b, ~np.asarray(masks[b], bool)] = -np.inf
     return y

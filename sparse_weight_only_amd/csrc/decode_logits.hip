@@ -75,10 +75,11 @@ __device__ __forceinline__ float penalised(float y, uint32_t w, float rep, float
 // the part (whole numbers, so the order of the atomics does not matter).
 // A bias list has few entries in a part (300 in 32 parts, say). The lanes that
 // hold them work out those logits themselves and write them once the part has
-// been written: of an id given twice the entry with the later place does, which
+// been written: of an id given twice the entry with the earlier place does, which
 // each lane knows from the part's entries in LDS (their order there does not
 // matter). A longer list, or more entries in one part, goes through a table of
-// places instead, by an atomic maximum, in the words of the counts (a table of
+// places instead, by an atomic maximum of the places from the end, in the words
+// of the counts (a table of
 // its own for every list cost a third of the waves of a compute unit: 93 us
 // for 256 x 128003 logits with 300 entries a row, 63 without any).
 // Bound by memory for a batch, by its round trips for one row: everything that
@@ -186,14 +187,14 @@ __global__ void __launch_bounds__(kLanes) logits_kernel(LogitsParams p) {
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) *(sgemv_dev::dword4*)&count[(s * kLanes + tid) * kPer] = sgemv_dev::dword4{0, 0, 0, 0};
     __syncthreads();
-    each_id(p.bias_ids, b0, b1, v0, n, [&](uint32_t v, int64_t i) { atomicMax(&count[v], (uint32_t)(i - b0) + 1u); });
+    each_id(p.bias_ids, b0, b1, v0, n, [&](uint32_t v, int64_t i) { atomicMax(&count[v], (uint32_t)(b1 - i)); });
     __syncthreads();
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       const sgemv_dev::dword4 w = *(const sgemv_dev::dword4*)&count[(s * kLanes + tid) * kPer];
 #pragma unroll
       for (int e = 0; e < kPer; ++e)
-        if (w[e]) l[s][e] += p.bias_values[b0 + w[e] - 1];
+        if (w[e]) l[s][e] += p.bias_values[b1 - w[e]];
     }
   }
 #pragma unroll
@@ -220,10 +221,10 @@ __global__ void __launch_bounds__(kLanes) logits_kernel(LogitsParams p) {
 #pragma unroll
     for (int k = 0; k < kShort; ++k) {
       if (mine[k] >= (uint32_t)n) continue;
-      bool last = true;
+      bool first = true;
       const uint32_t me = mine[k] << 16 | (uint32_t)(k * kLanes + tid);
-      for (int i = 0; i < n_listed; ++i) last &= listed[i] >> 16 != mine[k] || listed[i] <= me;
-      if (!last) continue;
+      for (int i = 0; i < n_listed; ++i) first &= listed[i] >> 16 != mine[k] || listed[i] >= me;
+      if (!first) continue;
       float y = logit[k];
       if (HIST) y = penalised(y, count[mine[k]], rep, freq, pres);
       out[mine[k]] = (TO)(bit[k] ? y + value[k] : -__builtin_inff());

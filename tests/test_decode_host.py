@@ -56,7 +56,7 @@ def test_oracle_logits_by_hand():
     x = np.array([[2.0, -2.0, 1.0, 0.0, 5.0]])
     y = odec.adjust_logits(x, [[0, 1, 1, 0, 4, 9, -1]], [3], [2.0], [0.5], [0.25], [[(2, 1.0), (2, 7.0)]], [[1, 1, 1, 1, 0]])
     # behind the prompt: 0 and 4 once each; 9 and -1 are no tokens
-    assert y.tolist() == [[1.0 - 0.75, -4.0, 8.0, 0.0, -np.inf]]
+    assert y.tolist() == [[1.0 - 0.75, -4.0, 2.0, 0.0, -np.inf]]
 
 
 # ------------------------------------------------------- frequency table

@@ -504,14 +504,14 @@ def test_logits(case, use):
 
 
 def test_logits_bias_given_twice():
-    """The last place holds, wherever the copies are in the list."""
+    """The first place holds, wherever the copies are in the list."""
     say("case bias twice")
     ids = np.array([5] * 700 + [9, 5, 9, 9, 4099, 4099])
-    vals = np.arange(len(ids)) * 0.5
+    vals = 1.0 + np.arange(len(ids)) * 0.5
     out = sg.adjust_logits(torch.zeros(1, 5000, device="cuda"), bias_ids=ints(ids), bias_values=torch.tensor(vals, dtype=F32, device="cuda"),
                            bias_start=ints([0, len(ids)]))
     want = np.zeros(5000)
-    want[5], want[9], want[4099] = vals[701], vals[703], vals[705]
+    want[5], want[9], want[4099] = vals[0], vals[700], vals[704]
     assert np.array_equal(host(out)[0], want)
 
 
