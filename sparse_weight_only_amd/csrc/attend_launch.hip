@@ -1,4 +1,5 @@
 // sgemv_attend_plan / sgemv_attend: host checks and the launches of the attention.
+#include "attend_few.hpp"
 #include "attend_join.hpp"
 #include "attend_kernels.hpp"
 #include "attend_many.hpp"
@@ -26,18 +27,21 @@ int make_shape(const sgemv_cache* c, const sgemv_seqs* s, int32_t tokens, int32_
   Shape h;
   h.dp = c->head_dim <= 64 ? 64 : c->head_dim <= 128 ? 128 : 256;
   const int64_t rows = (int64_t)tokens * group;
-  // Up to 32 rows a sequence on average: tiles of 16 rows that read K and V
-  // straight from memory, each tile for itself (27 candidates of 4 heads, 108
-  // rows: 55 us as 7 such tiles, 34 as one of 128). Up to 128: the tiles of 128.
-  h.few = rows <= (int64_t)32 * s->count;
-  h.waves = h.few ? (h.dp == 256 ? 4 : 8) : sgemv_dev::kManyWaves;
+  int64_t ctx = (int64_t)s->pages_per_seq * c->page_size;
+  if (max_ctx > 0 && max_ctx < ctx) ctx = max_ctx;
+  // Up to 16 rows a sequence on average: a tile of 16 that reads K and V
+  // straight from memory (12 rows, 4 sequences of up to 6000 slots, 8 heads:
+  // 20.5 us, 25.5 as a tile of 128). Up to 128 rows the same, a few tiles each
+  // for itself, over short contexts, where the larger kernel's start and end
+  // weigh more (96 rows over 300 slots: 9.7 against 15.2 us, over 6000: 61.6
+  // against 31.9; 48 rows: 11.9 against 13.6, and 39.5 against 27.8).
+  h.few = rows <= (int64_t)16 * s->count || (rows <= (int64_t)128 * s->count && ctx <= 1024);
+  h.waves = !h.few ? sgemv_dev::kManyWaves : h.dp == 256 ? sgemv_dev::kFewWaves<256> : sgemv_dev::kFewWaves<128>;
   h.halves = !h.few && h.dp < 256 && rows <= (int64_t)128 * s->count;
   h.tile_rows = h.few ? 16 : h.halves ? sgemv_dev::kManyRows<true> : sgemv_dev::kManyRows<false>;
   h.block = h.few || h.dp == 256 ? 32 : 64;
   h.lds = h.few ? 0 : h.dp == 64 ? sgemv_dev::kManyLds<64> : h.dp == 128 ? sgemv_dev::kManyLds<128> : sgemv_dev::kManyLds<256>;
   h.slots = rows / h.tile_rows + s->count;
-  int64_t ctx = (int64_t)s->pages_per_seq * c->page_size;
-  if (max_ctx > 0 && max_ctx < ctx) ctx = max_ctx;
   int64_t tiles = (rows + h.tile_rows - 1) / h.tile_rows;
   const int64_t each = s->count < tokens ? s->count : tokens;
   tiles = tiles < each ? each : tiles;
@@ -147,7 +151,7 @@ extern "C" int sgemv_attend(const sgemv_cache* cache, const sgemv_seqs* seqs, co
   p.scale2 = scale * 1.44269504088896340736f;
   p.part = (float*)workspace_dev;
   const bool bf16 = q->dtype == SGEMV_BF16;
-  sgemv_dev::AttendFn fn = h.few ? sgemv_dev::get_attend_few(bf16, p.dim, h.waves) : sgemv_dev::get_attend_many(bf16, p.dim, h.halves);
+  sgemv_dev::AttendFn fn = h.few ? sgemv_dev::get_attend_few(bf16, p.dim) : sgemv_dev::get_attend_many(bf16, p.dim, h.halves);
   (void)hipGetLastError();
   if (ensure_lds((const void*)fn, h.lds)) return SGEMV_EHIP;
   hipLaunchKernelGGL(fn, dim3((uint32_t)h.grid), dim3(64 * h.waves), (uint32_t)h.lds, (hipStream_t)hip_stream, p);

@@ -228,7 +228,7 @@ def test_nothing_to_do_is_no_launch():
 
 @pytest.mark.parametrize("tokens,heads,kv,dim,count,per_seq,max_ctx", [
     (1, 2, 2, 64, 1, 4, 0), (1, 8, 2, 128, 1, 8192, 0), (1, 8, 2, 128, 1, 8192, 300), (64, 32, 32, 128, 64, 100, 0), (4096, 32, 8, 128, 1, 256, 0),
-    (100, 8, 1, 256, 3, 4096, 0), (300, 3, 1, 80, 300, 7, 0)])
+    (100, 8, 1, 256, 3, 4096, 0), (300, 3, 1, 80, 300, 7, 0), (27, 8, 2, 128, 1, 400, 0), (27, 8, 2, 128, 1, 40, 0)])
 def test_plan(tokens, heads, kv, dim, count, per_seq, max_ctx):
     c = cache(heads=kv, head_dim=dim, k_page=16 * kv * dim, v_page=16 * kv * dim, k_slot=kv * dim, v_slot=kv * dim, k_head=dim, v_head=dim)
     pl = D.attend_plan(c, seqs(count=count, pages_per_seq=per_seq, pages_stride=per_seq), tokens, heads, max_ctx)

@@ -7,11 +7,14 @@ smallest FP16 subnormal (0 for BF16, whose range is FP32's):
 * append / rope: m (x cos - y sin): the angle's fraction of a turn to 2^-25 of
   a turn, 2 ulp of sine and cosine, four roundings: below 2^-20 m (|x| + |y|);
   then one rounding of the result: u |ref| + a.
-* attention: relative to A = sum p |v| / sum p: each p rounded once (u), the
-  result once (u), scores off by D e times sum |q k| scale on the first side
-  of the exponential and as much again for scale and maximum, so 2 D e S; the
-  sums over n keys, in any order, 2 n e; half subnormals of p, n a max |v|
-  (the largest p is 1 and enters the sum), and of the result, a.
+* attention: relative to A = sum p |v| / sum p: each p rounded once, in both
+  sums: with weights w_t summing to 1 and p_t (1 + d_t), |d_t| <= u, the result
+  moves by sum w d (v - o) / (1 + sum w d), at most u (A + |o|) <= 2 u A to
+  first order; the result rounded once (u A at most), so 3 u A; scores off by
+  D e times sum |q k| scale on the first side of the exponential and as much
+  again for scale and maximum, so 2 D e S; the sums over n keys, in any order,
+  2 n e; half subnormals of p, n a max |v| (the largest p is at least 1 and
+  enters the sum), and of the result, a.
 * logits: at most 6 FP32 operations on terms no larger than M = the sum of
   the magnitudes: 6 e M, then u |ref| + a (e |ref| for FP32).
 """
@@ -88,7 +91,7 @@ class Setup:
         big = np.abs(host(self.vc)[np.isfinite(host(self.vc))]).max()
         w = worst[:, :, None]
         n = keys[:, :, None]
-        return mean * (2 * u + 2 * self.dim * E * w + 2 * n * E) + n * a * big + a
+        return mean * (3 * u + 2 * self.dim * E * w + 2 * n * E) + n * a * big + a
 
     def check(self, out, want, what=""):
         ref = want[0]
@@ -233,6 +236,10 @@ ATTEND = [
     ([100, 30], [130, 640], 128, 5, 1, 112, F16, 0, 0, False, 0),
     ([50], [2000], 16, 3, 3, 40, F16, 0, 0, False, 2000),
     ([40], [512], 8, 16, 2, 24, BF16, 0, 0, False, 0),
+    ([33, 0, 7], [1500, 3, 1100], 16, 4, 2, 128, F16, 1, 1, False, 0),   # tiles of 128 rows, halves
+    ([100], [1300], 32, 1, 1, 64, BF16, 0, 0, True, 0),
+    ([25, 30], [2000, 1025], 8, 8, 2, 80, F16, 0, 0, False, 0),
+    ([20], [1200], 16, 4, 1, 256, F16, 0, 0, False, 0),
 ]
 
 
@@ -258,7 +265,7 @@ def test_attend(case):
 
 
 @pytest.mark.parametrize("scale", [1e-3, 0.5, 40.0])
-@pytest.mark.parametrize("n,heads", [(1, 2), (80, 2)])
+@pytest.mark.parametrize("n,heads", [(1, 2), (80, 2), (200, 1)])
 def test_attend_scales(scale, n, heads):
     """Weights from all equal to one key taking all."""
     say("case attend scale", scale, n)
@@ -267,7 +274,7 @@ def test_attend_scales(scale, n, heads):
     s.check(s.cache.attend(s.seqs, s.q, scale=scale), want, f"scale {scale}")
 
 
-TREE = [([7], [7]), ([27, 0, 33], [40, 5, 33]), ([3, 5], [200, 700]), ([64], [1500]), ([40], [72])]
+TREE = [([7], [7]), ([27, 0, 33], [40, 5, 33]), ([3, 5], [200, 700]), ([64], [1500]), ([40], [72]), ([27, 33], [1100, 90]), ([150], [190])]
 
 
 @pytest.mark.parametrize("n,ctx", TREE)
@@ -305,7 +312,7 @@ def test_attend_tree(n, ctx, kind, dim, heads, kv):
                 assert (host(out)[s.new_start[q]: s.new_start[q + 1]] == 0).all()
 
 
-@pytest.mark.parametrize("n,ctx,heads,kv", [([1, 1], [37, 300], 4, 2), ([3], [3], 2, 2), ([70, 33], [90, 333], 4, 2), ([200], [200], 1, 1)])
+@pytest.mark.parametrize("n,ctx,heads,kv", [([1, 1], [37, 300], 4, 2), ([3], [3], 2, 2), ([70, 33], [90, 333], 4, 2), ([200], [200], 1, 1), ([40, 40], [1090, 70], 4, 2)])
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), -65504.0])
 def test_attend_unseen_slots_have_no_part(n, ctx, heads, kv, value):
     """Slots behind a sequence's end, pages of nobody, and later tokens of the
@@ -336,7 +343,7 @@ def test_attend_unseen_slots_have_no_part(n, ctx, heads, kv, value):
         assert torch.isnan(got[last]).all(), "a row that sees NaN is NaN"
 
 
-@pytest.mark.parametrize("n,ctx", [([1], [200]), ([90], [200])])
+@pytest.mark.parametrize("n,ctx", [([1], [200]), ([90], [200]), ([90], [1200]), ([300], [400])])
 def test_attend_infinite_value_that_is_seen(n, ctx):
     """An infinite v is infinite for the rows that see it (all weights here are positive) and nothing for the others."""
     say("case infinite value", n)
@@ -350,7 +357,7 @@ def test_attend_infinite_value_that_is_seen(n, ctx):
 
 def test_attend_pages_that_are_not_there():
     say("case attend bad pages")
-    for n, ctx in (([1, 1, 2], [40, 100, 20]), ([70, 3], [100, 90])):
+    for n, ctx in (([1, 1, 2], [40, 100, 20]), ([70, 3], [100, 90]), ([70, 30], [100, 1090]), ([300, 3], [300, 90])):
         s = Setup(n, ctx, 16, 4, 2, 128, F16, 11)
         s.pages[0, 1], s.pages[1, 3], s.pages[1, 0] = -1, s.n_pages, 2 ** 31 - 1
         s.seqs = sg.Sequences(ints(s.new_start), ints(ctx), ints(s.pages))
@@ -364,7 +371,7 @@ def test_attend_pages_that_are_not_there():
 def test_attend_lengths_that_do_not_fit():
     """A context past its pages counts up to them; new tokens below slot 0 see nothing; a cache without pages."""
     say("case attend lengths")
-    for n, ctx, fit in (([1, 4], [200, 2], [64, 2]), ([80, 90], [10 ** 9, 70], [64, 64])):
+    for n, ctx, fit in (([1, 4], [200, 2], [64, 2]), ([80, 90], [10 ** 9, 70], [64, 64]), ([200, 190], [10 ** 9, 70], [64, 64])):
         s = Setup(n, [40, 64], 16, 2, 2, 64, F16, 12, per_seq=4)
         s.pages[:] = np.arange(8).reshape(2, 4) % s.n_pages
         s.ctx = fit
@@ -667,7 +674,7 @@ def test_decode_step_between_the_gemvs():
             assert (np.abs(got - ref) <= 2.0 ** -20 * 2 * mag + U[F16] * np.abs(ref) + A[F16]).all()
         a = cache.attend(seqs, q)
         out, mean, worst, keys = odec.attend(host(q), host(cache.k), host(cache.v), [0, 1, 2], [41 + step] * 2, pages.cpu().numpy(), dim ** -0.5)
-        tol = mean * (2 * U[F16] + 2 * dim * E * worst[:, :, None] + 2 * keys[:, :, None] * E) + (41 + step) * A[F16] * 8 + A[F16]
+        tol = mean * (3 * U[F16] + 2 * dim * E * worst[:, :, None] + 2 * keys[:, :, None] * E) + (41 + step) * A[F16] * 8 + A[F16]
         assert (np.abs(host(a) - out) <= tol).all()
         x = wo.run(a.reshape(B, hidden))
         logits = wh.run(x)
