@@ -11,7 +11,7 @@ import pytest
 
 import sparse_weight_only_amd as sg
 from oracle import decode as odec
-from sparse_weight_only_amd import _build, _build_san, decode as D
+from sparse_weight_only_amd import _build, decode as D
 from sparse_weight_only_amd.sgemv import SGEMV_EALIGN, SGEMV_EINVAL, SGEMV_ESIZE
 
 torch = pytest.importorskip("torch")
@@ -82,6 +82,7 @@ def test_rope_table_refusals(args):
 # ------------------------------------------------------- index arithmetic
 
 def test_index_arithmetic_under_sanitizers():
+    from sparse_weight_only_amd import _build_san
     exe = _build_san.INDEX_CHECK
     newest = max(os.path.getmtime(f) for f in (_build_san.INDEX_SRC, os.path.join(_build.CSRC, "decode_index.hpp")))
     if not os.path.exists(exe) or os.path.getmtime(exe) < newest:
