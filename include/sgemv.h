@@ -382,7 +382,8 @@ typedef struct sgemv_rows {
 /* A paged cache of keys and values: element (page, slot, head, column) of K
  * at k[page * k_page + slot * k_slot + head * k_head + column], and of V
  * likewise. Alignment and strides as sgemv_rows. page_size: a power of two,
- * 8..65536 slots. */
+ * 8..65536 slots. sgemv_attend takes page strides below 2^31 and slot strides
+ * below 2^27 (ESIZE beyond); head strides, offsets and sizes are 64 bits wide. */
 typedef struct sgemv_cache {
   void *k, *v;
   int64_t k_page, k_slot, k_head;
