@@ -13,6 +13,7 @@ stream that it runs on.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import numpy as np
 
@@ -106,17 +107,26 @@ def _ref(x):
     return None if x is None else _byref(x)
 
 
+def _packer(structure):
+    """A function from a structure's fields to its bytes, which cost a quarter of what the structure does."""
+    codes = {_P: "P", _I64: "q", _I32: "i"}
+    return struct.Struct("@" + "".join(codes[t] for _, t in structure._fields_) + "0q").pack
+
+
+_pack_rows, _pack_logits = _packer(Rows), _packer(Logits)
+
 # torch and what is looked up in it on every call, set by _init (the library's
 # host side is used without torch)
-torch = _types = _raw_stream = None
+torch = _types = _raw_stream = _current_device = None
 
 
 def _init():
-    global torch, _types, _raw_stream
+    global torch, _types, _raw_stream, _current_device
     import torch as t
     _types = {t.float16: F16, t.bfloat16: BF16, t.float32: F32}
     # the raw current stream without building a Stream object, which costs more than the rest of a call's checks
     _raw_stream = getattr(t._C, "_cuda_getCurrentRawStream", None) or (lambda i: t.cuda.current_stream(i).cuda_stream)
+    _current_device = getattr(t._C, "_cuda_getDevice", None) or t.cuda.current_device
     torch = t
 
 
@@ -127,17 +137,23 @@ def _type(dtype) -> int:
         raise ValueError(f"no operator for {dtype}") from None
 
 
-def _rows(x, what: str) -> Rows:
-    if x.dim() != 3:
-        raise ValueError(f"{what} must be [tokens, heads, head_dim]")
+def _rows(x, what: str) -> bytes:
+    """The bytes of a Rows."""
+    try:
+        t, h, d = x.shape
+    except ValueError:
+        raise ValueError(f"{what} must be [tokens, heads, head_dim]") from None
     st, sh, sd = x.stride()
-    t, h, d = x.shape
     if sd != 1 and d > 1:
         raise ValueError(f"{what} must have contiguous columns")
-    return Rows(x.data_ptr(), st, sh, t, h, d, _type(x.dtype))
+    dtype = _types.get(x.dtype)
+    if dtype is None:
+        dtype = _type(x.dtype)
+    return _pack_rows(x.data_ptr(), st, sh, t, h, d, dtype)
 
 
 def _on(device, **tensors) -> None:
+    # a call asks each tensor's get_device() first, at half the cost, and comes here to say which one differs
     for what, x in tensors.items():
         if x is not None and x.device != device:
             raise ValueError(f"{what} is on {x.device}, not on {device}")
@@ -156,7 +172,7 @@ def _enter(device, stream):
         raise ValueError(f"tensors are on {device}, not on a GPU")
     i = device.index
     if stream is None:
-        if torch.cuda.current_device() == i:
+        if _current_device() == i:
             return _raw_stream(i), None
         ctx = torch.cuda.device(i)
         ctx.__enter__()
@@ -186,6 +202,7 @@ class Rope:
         _init()
         self.turns = torch.from_numpy(rope_table(rot_dim, base, factor, context, low, high)).to(device)
         self.args = RopeArgs(self.turns.data_ptr(), rot_dim, int(bool(interleaved)), magnitude)
+        self._ref, self._index = _byref(self.args), self.turns.get_device()
 
     def apply(self, x, positions, out=None, stream=None):
         """x [tokens, heads, head_dim] turned at ``positions`` (int32 [tokens]) into ``out`` (a new tensor; x itself is fine)."""
@@ -196,9 +213,11 @@ class Rope:
         try:
             if out is None:
                 out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-            rope(self.args, positions.data_ptr(), xr, _rows(out, "out"), s)
+            code = lib().sgemv_rope(self._ref, positions.data_ptr(), xr, _rows(out, "out"), s)
         finally:
             _leave(ctx)
+        if code:
+            _check(code, "sgemv_rope")
         return out
 
 
@@ -222,6 +241,7 @@ class Sequences:
         self.new_start, self.ctx_len, self.pages = new_start, ctx_len, pages
         self.device = ctx_len.device
         self.args = Seqs(new_start.data_ptr(), ctx_len.data_ptr(), pages.data_ptr(), pages.stride(0), count, pages.shape[1])
+        self._ref, self._index = _byref(self.args), ctx_len.get_device()
 
 
 class PagedCache:
@@ -252,6 +272,7 @@ class PagedCache:
         _on(k.device, v=v)
         self.k, self.v, self.device = k, v, k.device
         self.args = Cache(k.data_ptr(), v.data_ptr(), *k.stride()[:3], *v.stride()[:3], *k.shape, _type(k.dtype))
+        self._ref, self._index = _byref(self.args), k.get_device()
 
     def append(self, seqs: Sequences, k, v, rope: Rope = None, q=None, q_out=None, positions=None, stream=None):
         """Store the new tokens' k (turned by ``rope``) and v, [tokens, heads,
@@ -262,18 +283,25 @@ class PagedCache:
             raise ValueError("q and positions need a rope")
         if q is None and q_out is not None:
             raise ValueError("q_out needs q")
-        dev = self.device
+        dev, i = self.device, self._index
+        at = qr = qo = None
         if positions is not None:
             _ints(positions, "positions", (k.shape[0],))
-        _on(dev, k=k, v=v, q=q, q_out=q_out, positions=positions, seqs=seqs, rope=rope and rope.turns)
-        qr, kr, vr = None if q is None else _ref(_rows(q, "q")), _rows(k, "k"), _rows(v, "v")
+            at = positions.data_ptr()
+        if (k.get_device() != i or v.get_device() != i or seqs._index != i or (q is not None and q.get_device() != i)
+                or (q_out is not None and q_out.get_device() != i) or (rope is not None and rope._index != i)
+                or (at is not None and positions.get_device() != i)):
+            _on(dev, k=k, v=v, q=q, q_out=q_out, positions=positions, seqs=seqs, rope=rope and rope.turns)
+        if q is not None:
+            qr = _rows(q, "q")
+        kr, vr = _rows(k, "k"), _rows(v, "v")
         s, ctx = _enter(dev, stream)
         try:
-            if q is not None and q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            code = lib().sgemv_append(_ref(self.args), _ref(seqs.args), None if rope is None else _ref(rope.args),
-                                      0 if positions is None else positions.data_ptr(), qr,
-                                      None if q is None else _ref(_rows(q_out, "q_out")), _ref(kr), _ref(vr), s)
+            if q is not None:
+                if q_out is None:
+                    q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+                qo = _rows(q_out, "q_out")
+            code = lib().sgemv_append(self._ref, seqs._ref, None if rope is None else rope._ref, at, qr, qo, kr, vr, s)
         finally:
             _leave(ctx)
         if code:
@@ -295,7 +323,7 @@ class PagedCache:
         more, not shared with calls that may run at the same time; made if
         not given. Rows of no sequence stay as they are in a given ``out``
         and are undefined in a new one."""
-        dev = self.device
+        dev, i = self.device, self._index
         words = at = 0
         if tree is not None:
             _ints(tree, "tree")
@@ -304,23 +332,26 @@ class PagedCache:
             words, at = tree.shape[1], tree.data_ptr()
         if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
             raise ValueError("workspace must be a contiguous uint8 tensor")
-        _on(dev, q=q, seqs=seqs, tree=tree, out=out, workspace=workspace)
+        if (q.get_device() != i or seqs._index != i or (out is not None and out.get_device() != i)
+                or (tree is not None and tree.get_device() != i) or (workspace is not None and workspace.get_device() != i)):
+            _on(dev, q=q, seqs=seqs, tree=tree, out=out, workspace=workspace)
         qr = _rows(q, "q")
+        tokens, heads, dim = q.shape
         s, ctx = _enter(dev, stream)
         try:
             if out is None:
                 out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-            L, c, sq = lib(), _ref(self.args), _ref(seqs.args)
+            L, c, sq = lib(), self._ref, seqs._ref
             if workspace is None:
                 pl = AttendPlan()
-                code = L.sgemv_attend_plan(c, sq, qr.tokens, qr.heads, max_ctx, _ref(pl))
+                code = L.sgemv_attend_plan(c, sq, tokens, heads, max_ctx, _byref(pl))
                 if code:
                     _check(code, "sgemv_attend_plan")
                 if pl.workspace_bytes:
                     workspace = torch.empty(pl.workspace_bytes, dtype=torch.uint8, device=dev)
             scratch, room = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
-            code = L.sgemv_attend(c, sq, _ref(qr), _ref(_rows(out, "out")), qr.head_dim ** -0.5 if scale is None else scale,
-                                  at, words, max_ctx, scratch, room, s)
+            code = L.sgemv_attend(c, sq, qr, _rows(out, "out"), dim ** -0.5 if scale is None else scale, at, words, max_ctx,
+                                  scratch, room, s)
         finally:
             _leave(ctx)
         if code:
@@ -341,7 +372,7 @@ def adjust_logits(x, out=None, history=None, history_start=None, prompt_len=None
     allowed; mask_row (int32 [rows]): each row's mask, -1 for none."""
     if torch is None:
         _init()
-    dev = x.device
+    dev, card = x.device, x.get_device()
     rows, vocab = x.shape if x.dim() == 2 else (-1, -1)
     sx, cx = x.stride() if rows >= 0 else (0, 0)
     if rows < 0 or (cx != 1 and vocab > 1):
@@ -350,48 +381,50 @@ def adjust_logits(x, out=None, history=None, history_start=None, prompt_len=None
         raise ValueError(f"out must have the shape of x, and contiguous rows, on {dev}")
 
     def at(t, what, n, dtype):
-        if t.dtype != dtype or t.shape != n or not t.is_contiguous() or t.device != dev:
+        if t.dtype != dtype or t.shape != n or not t.is_contiguous() or t.get_device() != card:
             raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {list(n)} on {dev}")
         return t.data_ptr()
 
     i32, f32 = torch.int32, torch.float32
     one, ends = (rows,), (rows + 1,)
-    g = Logits(x.data_ptr(), 0, sx, 0)
-    g.rows, g.vocab, g.dtype = rows, vocab, _type(x.dtype)
+    hist_start = hist_ids = n_hist = prompt = rep = freq = pres = 0
+    b_start = b_ids = b_values = n_bias = mask_at = mask_stride = mask_rows = n_masks = 0
     if history is not None or history_start is not None:
         if history is None or history_start is None:
             raise ValueError("history and history_start belong together")
         n = history.numel()
-        g.hist_ids, g.hist_start, g.n_hist = at(history, "history", (n,), i32), at(history_start, "history_start", ends, i32), n
+        hist_ids, hist_start, n_hist = at(history, "history", (n,), i32), at(history_start, "history_start", ends, i32), n
     if prompt_len is not None:
-        g.prompt_len = at(prompt_len, "prompt_len", one, i32)
+        prompt = at(prompt_len, "prompt_len", one, i32)
     if repetition is not None:
-        g.repetition = at(repetition, "repetition", one, f32)
+        rep = at(repetition, "repetition", one, f32)
     if frequency is not None:
-        g.frequency = at(frequency, "frequency", one, f32)
+        freq = at(frequency, "frequency", one, f32)
     if presence is not None:
-        g.presence = at(presence, "presence", one, f32)
+        pres = at(presence, "presence", one, f32)
     if bias_ids is not None or bias_values is not None or bias_start is not None:
         if bias_ids is None or bias_values is None or bias_start is None:
             raise ValueError("bias_ids, bias_values and bias_start belong together")
         n = bias_ids.numel()
-        g.bias_ids, g.bias_values, g.n_bias = at(bias_ids, "bias_ids", (n,), i32), at(bias_values, "bias_values", (n,), f32), n
-        g.bias_start = at(bias_start, "bias_start", ends, i32)
+        b_ids, b_values, n_bias = at(bias_ids, "bias_ids", (n,), i32), at(bias_values, "bias_values", (n,), f32), n
+        b_start = at(bias_start, "bias_start", ends, i32)
     if masks is not None:
         words = (vocab + 31) // 32
         if masks.dtype != i32 or masks.dim() != 2 or masks.shape[1] != words or (words > 1 and masks.stride(1) != 1) or masks.device != dev:
             raise ValueError(f"masks must be an int32 tensor of shape [n, {words}] with contiguous rows on {dev}")
-        g.masks, g.mask_stride, g.n_masks = masks.data_ptr(), masks.stride(0), masks.shape[0]
+        mask_at, mask_stride, n_masks = masks.data_ptr(), masks.stride(0), masks.shape[0]
         if mask_row is not None:
-            g.mask_row = at(mask_row, "mask_row", one, i32)
+            mask_rows = at(mask_row, "mask_row", one, i32)
     elif mask_row is not None:
         raise ValueError("mask_row needs masks")
     s, ctx = _enter(dev, stream)
     try:
         if out is None:
             out = torch.empty(x.shape, dtype=f32, device=dev)
-        g.out, g.out_stride, g.out_dtype = out.data_ptr(), out.stride(0), _type(out.dtype)
-        code = lib().sgemv_adjust_logits(ctypes.byref(g), s)
+        g = _pack_logits(x.data_ptr(), out.data_ptr(), sx, out.stride(0), hist_start, hist_ids, n_hist, prompt, rep, freq, pres,
+                         b_start, b_ids, b_values, n_bias, mask_at, mask_stride, mask_rows, n_masks, rows, vocab, _type(x.dtype),
+                         _type(out.dtype))
+        code = lib().sgemv_adjust_logits(g, s)
     finally:
         _leave(ctx)
     if code:

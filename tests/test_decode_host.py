@@ -287,6 +287,15 @@ def ints(*shape):
     return t(*shape, dtype=torch.int32)
 
 
+def test_packed_structures():
+    for structure, pack in ((D.Rows, D._pack_rows), (D.Logits, D._pack_logits)):
+        values = [(7 << 33) + 3 * i if t is not ctypes.c_int32 else 5 - 2 * i for i, (_, t) in enumerate(structure._fields_)]
+        packed = pack(*values)
+        assert len(packed) == ctypes.sizeof(structure)
+        got = structure.from_buffer_copy(packed)
+        assert [getattr(got, f) for f, _ in structure._fields_] == values
+
+
 def test_binding_refuses_what_it_cannot_pass_on():
     c = sg.PagedCache(4, 16, 2, 64, device="cpu")
     s = sg.Sequences(ints(3), ints(2), ints(2, 4))
