@@ -571,6 +571,39 @@ def test_logits_lists_that_do_not_fit():
     assert np.array_equal(out, want)
 
 
+# ------------------------------------------- tensors of another device
+
+def test_tensors_on_the_cpu_are_refused_by_name():
+    say("case cpu tensors")
+    s = Setup([1, 3], [40, 70], 16, 4, 2, 64, F16, 23)
+    cpu = lambda x: x.detach().cpu()
+    rope, far = sg.Rope(64), sg.Rope(64, device="cpu")
+    pos = ints([0, 1, 2, 3])
+    tree = ints(np.zeros((4, 1)))
+    there = sg.Sequences(cpu(s.seqs.new_start), cpu(s.seqs.ctx_len), cpu(s.seqs.pages))
+    good = dict(seqs=s.seqs, k=s.k, v=s.v, rope=rope, q=s.q, q_out=torch.empty_like(s.q), positions=pos)
+    for what, x in (("seqs", there), ("k", cpu(s.k)), ("v", cpu(s.v)), ("rope", far), ("q", cpu(s.q)), ("q_out", cpu(s.q)), ("positions", cpu(pos))):
+        with pytest.raises(ValueError, match=f"{what} is on cpu"):
+            s.cache.append(**{**good, what: x})
+    work = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    good = dict(seqs=s.seqs, q=s.q, tree=tree, out=torch.empty_like(s.q), workspace=work)
+    for what, x in (("seqs", there), ("q", cpu(s.q)), ("tree", cpu(tree)), ("out", cpu(s.q)), ("workspace", cpu(work))):
+        with pytest.raises(ValueError, match=f"{what} is on cpu"):
+            s.cache.attend(**{**good, what: x})
+    for what, args in (("x", (cpu(s.q), pos)), ("positions", (s.q, cpu(pos))), ("out", (s.q, pos, cpu(s.q)))):
+        with pytest.raises(ValueError, match=f"{what} is on cpu"):
+            rope.apply(*args)
+    x = torch.zeros(2, 50, device="cuda")
+    lists = dict(history=ints([1, 2]), history_start=ints([0, 1, 2]), prompt_len=ints([1, 1]), repetition=torch.ones(2, device="cuda"),
+                 frequency=torch.ones(2, device="cuda"), presence=torch.ones(2, device="cuda"), bias_ids=ints([3]), bias_start=ints([0, 0, 1]),
+                 bias_values=torch.ones(1, device="cuda"), masks=ints([[-1, -1]]), mask_row=ints([0, -1]))
+    for what in lists:
+        with pytest.raises(ValueError, match=what):
+            sg.adjust_logits(x, **{**lists, what: cpu(lists[what])})
+    with pytest.raises(ValueError, match="out"):
+        sg.adjust_logits(x, out=cpu(x), **lists)
+
+
 # ------------------------------------------- streams, graphs, use together
 
 def test_other_stream_and_two_at_once():
