@@ -46,8 +46,8 @@ int make_shape(const sgemv_cache* c, const sgemv_seqs* s, int32_t tokens, int32_
   const int64_t each = s->count < tokens ? s->count : tokens;
   tiles = tiles < each ? each : tiles;
   // Workgroups to aim for: one a compute unit, as a workgroup has eight waves
-  // and up to 128 KiB of LDS; two of the 64-column kernel fit (a chunk of 777
-  // and one of 544 over up to 9001: 71 us, 76 with one). More parts than that
+  // and up to 128 KiB of LDS; two of the 64-column kernel fit (chunks of 777
+  // over 9001 and 440 over 4550: 71 us, 76 with one). More parts than that
   // only add to what is joined (131071 slots, 8 heads: 100 us with 256, 102
   // with 512, 107 with 1024). A part has two blocks at least in the few-row
   // kernel (700 slots, 32 heads: 10.0 us with parts of 64, 11.0 of 128, 12.8
