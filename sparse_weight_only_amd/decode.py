@@ -329,7 +329,8 @@ class PagedCache:
             _ints(tree, "tree")
             if tree.dim() != 2 or tree.shape[0] != q.shape[0]:
                 raise ValueError("tree must be [tokens, words]")
-            words, at = tree.shape[1], tree.data_ptr()
+            # a tree without words has no address, which would mean no tree; nothing is read of it
+            words, at = tree.shape[1], tree.data_ptr() or seqs.new_start.data_ptr()
         if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
             raise ValueError("workspace must be a contiguous uint8 tensor")
         if (q.get_device() != i or seqs._index != i or (out is not None and out.get_device() != i)

@@ -1,0 +1,48 @@
+"""Decode-step operators where they can go wrong between the cases of the parity
+tests. Tolerances as those count them (u the type's half step, e = 2^-24),
+except where a test counts its own.
+"""
+import numpy as np
+import pytest
+
+import sparse_weight_only_amd as sg
+from gpu_util import say
+from test_gpu_decode import F16, Setup, host, ints
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    sg.lib()
+
+
+# ---------------------------------------------------------- empty tensors
+
+@pytest.mark.parametrize("n,ctx", [([4], [4]), ([3, 0, 5], [40, 7, 5]), ([90], [100]), ([40], [1100])])
+def test_tree_without_words(n, ctx):
+    """No word: no new token sees a new token, as bits past the words count as 0."""
+    say("case tree without words", n, ctx)
+    s = Setup(n, ctx, 16, 4, 2, 64, F16, 31)
+    want = s.want(tree=np.zeros((s.tokens, 0), np.uint32))
+    out = s.cache.attend(s.seqs, s.q, tree=torch.zeros(s.tokens, 0, dtype=torch.int32, device="cuda"))
+    s.check(out, want, "no words")
+    for q in range(len(n)):
+        if n[q] == ctx[q]:
+            assert (host(out)[s.new_start[q]: s.new_start[q + 1]] == 0).all()
+
+
+def test_no_tokens():
+    """Nothing is done, whatever else is given."""
+    say("case no tokens")
+    cache = sg.PagedCache(4, 16, 2, 64)
+    seqs = sg.Sequences(ints([0, 0]), ints([5]), ints([[0]]))
+    none = torch.zeros(0, 2, 64, dtype=F16, device="cuda")
+    for words in (0, 2):
+        assert cache.attend(seqs, none, tree=torch.zeros(0, words, dtype=torch.int32, device="cuda")).shape == (0, 2, 64)
+    rope, at = sg.Rope(64), ints([])
+    assert cache.append(seqs, none, none, rope=rope, q=none, positions=at).shape == (0, 2, 64)
+    assert rope.apply(none, at).shape == (0, 2, 64)
