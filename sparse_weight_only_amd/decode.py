@@ -413,9 +413,14 @@ def adjust_logits(x, out=None, history=None, history_start=None, prompt_len=None
         words = (vocab + 31) // 32
         if masks.dtype != i32 or masks.dim() != 2 or masks.shape[1] != words or (words > 1 and masks.stride(1) != 1) or masks.device != dev:
             raise ValueError(f"masks must be an int32 tensor of shape [n, {words}] with contiguous rows on {dev}")
-        mask_at, mask_stride, n_masks = masks.data_ptr(), masks.stride(0), masks.shape[0]
         if mask_row is not None:
             mask_rows = at(mask_row, "mask_row", one, i32)
+        # empty tensors have no address, which would mean that there are none: rows without their masks, masks without
+        # their rows
+        if rows and masks.shape[0] == 0:
+            raise ValueError(f"masks holds no mask for {rows} rows")
+        if rows or mask_row is None:
+            mask_at, mask_stride, n_masks = masks.data_ptr(), masks.stride(0), masks.shape[0]
     elif mask_row is not None:
         raise ValueError("mask_row needs masks")
     s, ctx = _enter(dev, stream)

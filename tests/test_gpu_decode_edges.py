@@ -46,3 +46,26 @@ def test_no_tokens():
     rope, at = sg.Rope(64), ints([])
     assert cache.append(seqs, none, none, rope=rope, q=none, positions=at).shape == (0, 2, 64)
     assert rope.apply(none, at).shape == (0, 2, 64)
+
+
+def test_no_rows():
+    """Nothing is done, whatever else is given."""
+    say("case no rows")
+    x, masks = torch.zeros(0, 50, device="cuda"), ints([[-1, -1], [3, 0]])
+    empty = torch.zeros(0, device="cuda")
+    for kw in (dict(masks=masks, mask_row=ints([])), dict(masks=masks[:0]), dict(masks=masks[:0], mask_row=ints([])),
+               dict(history=ints([]), history_start=ints([0]), prompt_len=ints([]), repetition=empty, frequency=empty, presence=empty),
+               dict(bias_ids=ints([]), bias_values=empty, bias_start=ints([0]))):
+        assert sg.adjust_logits(x, **kw).shape == (0, 50)
+
+
+def test_mask_tables_that_are_empty_or_short_are_refused():
+    """A row without its mask would be left unmasked."""
+    say("case short mask tables")
+    x, masks = torch.zeros(3, 50, device="cuda"), torch.zeros(5, 2, dtype=torch.int32, device="cuda")
+    for m in (masks[:0], masks[:2], masks[:4]):
+        with pytest.raises(ValueError if len(m) == 0 else sg.SgemvError):
+            sg.adjust_logits(x, masks=m)
+    with pytest.raises(ValueError, match="no mask"):
+        sg.adjust_logits(x, masks=masks[:0], mask_row=ints([0, 0, 0]))
+    assert np.isneginf(host(sg.adjust_logits(x, masks=masks[:3]))).all()
