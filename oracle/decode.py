@@ -79,8 +79,8 @@ def attend(q, k_cache, v_cache, new_start, ctx_len, pages, scale, tree=None):
             if tree is None:
                 ok = t <= old + i
             else:
-                j = t - old
-                ok = j < 0 or (j < 32 * tree.shape[1] and bool(int(tree[row, j // 32]) >> (j % 32) & 1))
+                j = t - old                  # a token below slot 0 sees nothing, whatever its bits
+                ok = old + i >= 0 and (j < 0 or (j < 32 * tree.shape[1] and bool(int(tree[row, j // 32]) >> (j % 32) & 1)))
             if ok:
                 see.append((int(pages[s, t // page]), t % page))
         out[row] = 0.0

@@ -30,16 +30,19 @@ def asan_runtime() -> str:
 
 
 # The decode-step operators' index arithmetic (csrc/decode_index.hpp, shared
-# with the kernels) as a program of its own for the CPU tests.
+# with the kernels) as programs of their own for the CPU tests.
 _INDEX_DIR = os.path.join(os.path.dirname(os.path.dirname(CSRC)), "tests", "decode_index")
 INDEX_SRC = os.path.join(_INDEX_DIR, "index_check.cpp")
 INDEX_CHECK = os.path.join(_INDEX_DIR, "_build", "index_check")
+VISIBLE_SRC = os.path.join(_INDEX_DIR, "visible_check.cpp")
+VISIBLE_CHECK = os.path.join(_INDEX_DIR, "_build", "visible_check")
 
 
 def build_index_check(verbose: bool = False) -> str:
     os.makedirs(os.path.dirname(INDEX_CHECK), exist_ok=True)
-    tmp = INDEX_CHECK + ".tmp"
-    _run(["g++", "-std=c++17", "-O1", "-g", "-fno-omit-frame-pointer", "-fsanitize=address,undefined",
-          "-fno-sanitize-recover=all", "-Wall", "-Wextra", INDEX_SRC, "-o", tmp], verbose)
-    os.replace(tmp, INDEX_CHECK)
+    for src, exe in ((INDEX_SRC, INDEX_CHECK), (VISIBLE_SRC, VISIBLE_CHECK)):
+        tmp = exe + ".tmp"
+        _run(["g++", "-std=c++17", "-O1", "-g", "-fno-omit-frame-pointer", "-fsanitize=address,undefined",
+              "-fno-sanitize-recover=all", "-Wall", "-Wextra", src, "-o", tmp], verbose)
+        os.replace(tmp, exe)
     return INDEX_CHECK

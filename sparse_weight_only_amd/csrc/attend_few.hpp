@@ -120,7 +120,7 @@ struct Few {
     for (int e = 0; e < 8; ++e) s[e] = a[e / 4][e % 4];
     if (kb + kFewBlock > t.full || b.there != ~0u) {
       const int row = t.row0 + r < t.rows ? t.row0 + r : t.rows - 1;
-      const uint32_t bits = seen_bits(p, t, row / p.group, kb) & b.there;
+      const uint32_t bits = visible_bits(p, t, row / p.group, kb) & b.there;
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         if (!(bits >> (16 * (e / 4) + 4 * g + e % 4) & 1u)) s[e] = -__builtin_inff();

@@ -147,7 +147,7 @@ struct Many {
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
       const int at = 32 * (i + part);
-      const uint32_t bits = (seen_bits(p, t, row / p.group, kb + at) & (uint32_t)(there >> at)) >> (4 * h);
+      const uint32_t bits = (visible_bits(p, t, row / p.group, kb + at) & (uint32_t)(there >> at)) >> (4 * h);
 #pragma unroll
       for (int e = 0; e < 16; ++e)
         if (!(bits >> (8 * (e / 4) + e % 4) & 1u)) s[i][e] = -__builtin_inff();
@@ -268,7 +268,7 @@ struct Many {
         const int d = 16 * j + 8 * h;
         x = Half<T>::mma32(load<dword4>(or_nothing(ok && (WHOLE || d < p.dim), addr(kr + d))), q[j], x);
       }
-      const uint32_t bits = seen_bits(p, t, row / p.group, kb) & there;
+      const uint32_t bits = visible_bits(p, t, row / p.group, kb) & there;
       for (int key = 0; key < 32; ++key) {
         // this key's score for row c, from the half that holds it
         const int e = key / 8 * 4 + key % 4;

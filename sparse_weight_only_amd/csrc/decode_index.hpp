@@ -116,7 +116,8 @@ SGEMV_BOTH bool make_tile(const TileView& p, int m, int block, int s, int first,
   return true;
 }
 
-// Bit b: whether new token `i` of the tile's sequence sees key kb + b.
+// Bit b: whether key kb + b lies before the end and new token `i` of the tile's
+// sequence sees it, by its slot or by its words of the tree.
 SGEMV_BOTH uint32_t seen_bits(const TileView& p, const Tile& t, int i, int kb) {
   int n;
   uint32_t bits = ~0u;
@@ -134,6 +135,14 @@ SGEMV_BOTH uint32_t seen_bits(const TileView& p, const Tile& t, int i, int kb) {
     n = n < t.end - kb ? n : t.end - kb;
   }
   return n >= 32 ? bits : n <= 0 ? 0u : bits & ((1u << n) - 1u);
+}
+
+// The same for a token that may have no slot: in a sequence shorter than its
+// new tokens the first of them lie below slot 0 and see no key, whatever their
+// words of the tree say. Such a tile has `full` at 0 or less, so all of its
+// blocks are masked.
+SGEMV_BOTH uint32_t visible_bits(const TileView& p, const Tile& t, int i, int kb) {
+  return t.old + i < 0 ? 0u : seen_bits(p, t, i, kb);
 }
 
 }  // namespace sgemv_dev

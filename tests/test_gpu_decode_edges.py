@@ -69,3 +69,20 @@ def test_mask_tables_that_are_empty_or_short_are_refused():
     with pytest.raises(ValueError, match="no mask"):
         sg.adjust_logits(x, masks=masks[:0], mask_row=ints([0, 0, 0]))
     assert np.isneginf(host(sg.adjust_logits(x, masks=masks[:3]))).all()
+
+
+# ------------------------------------------- candidates below slot 0
+
+@pytest.mark.parametrize("n,ctx", [([4], [2]), ([4, 2, 3], [2, 30, 0]), ([70, 3], [60, 90]), ([300], [17]), ([40, 30], [1090, 9])])
+def test_candidates_below_slot_zero_see_nothing(n, ctx):
+    """Lengths shorter than the new tokens: those without a slot get zeros, the others what their bits say."""
+    say("case tree below slot 0", n, ctx)
+    per = -(-max(ctx + [1]) // 16)
+    s = Setup(n, ctx, 16, 4, 2, 64, F16, 32, per_seq=per)
+    words = (max(n) + 31) // 32
+    tree = np.random.default_rng(33).integers(0, 2 ** 32, (s.tokens, words), dtype=np.uint32)
+    out = s.cache.attend(s.seqs, s.q, tree=torch.from_numpy(tree.view(np.int32)).cuda())
+    s.check(out, s.want(tree=tree), "below slot 0")
+    for q in range(len(n)):
+        a = int(s.new_start[q])
+        assert (host(out)[a: a + max(0, n[q] - ctx[q])] == 0).all(), "a token without a slot saw a key"
