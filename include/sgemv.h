@@ -496,9 +496,11 @@ int sgemv_attend_plan(const sgemv_cache* cache, const sgemv_seqs* seqs, int32_t 
  * no part in its result, whatever it holds (infinities and NaN included), and
  * so have slots behind a sequence's end.
  * Numerics: scores, the running maximum, sums and outputs in FP32; each p_t
- * relative to the row's maximum rounded to the cache's type; one rounding at
- * the end: |out - exact| <= about (3 u + e) max_t |V[t]| with u the type's
- * half step and e FP32's over the scores' size. Deterministic for one plan.
+ * relative to the row's maximum rounded to the cache's type (in FP16 those
+ * under 2^-32 of the largest count as 0); one rounding at the end:
+ * |out - exact| <= about (3 u + 2 e (head_dim S + n)) max_t |V[t]| with u the
+ * type's half step, e = 2^-24, S the largest scale sum_d |q_d K[t]_d| of the
+ * row and n its visible keys. Deterministic for one plan.
  * Enqueues one kernel, or two with splits, and returns without synchronising.
  * out overlaps nothing else. Errors: EINVAL, EALIGN, ESIZE (sizes beyond the
  * grid, workspace too small), EHIP. */

@@ -41,7 +41,7 @@ struct Few {
   int r, g;                               // lane = r + 16 g
   dword4 q[KC];
   f32x4 o[VC];
-  float m, l;                             // running maximum and this lane's share of the sum
+  float m, l;                             // where the weights are 1 (kLift below the maximum), and this lane's share of the sum
 
   __device__ __forceinline__ Few(const AttendParams& p_, const Tile& t_, int head) : p(p_), t(t_) {
     const int lane = threadIdx.x & 63;
@@ -131,7 +131,7 @@ struct Few {
     float s[8];
     scores(kb, b, s);
     float top = fmaxf(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])), fmaxf(fmaxf(s[4], s[5]), fmaxf(s[6], s[7])));
-    top = max_x32(max_x16(top)) * p.scale2;
+    top = __builtin_fmaf(max_x32(max_x16(top)), p.scale2, -Half<T>::kLift);
     if (__any(top > m + kSlack)) {
       const float to = fmaxf(m, top), by = m == to ? 1.0f : exp2_fast(m - to);
       l *= by;

@@ -179,14 +179,14 @@ struct Many {
       for (int i = 0; i < NS; ++i) s[i] = Half<T>::mma32(lds_load((32 * j ^ mix) + row + 32 * i * DP * 2), q[j], s[i]);
   }
 
-  // w = the weights of the block at kb from its scores, and the running
-  // maximum and sum with it
+  // w = the weights of the block at kb from its scores, and m and the sum with
+  // it
   __device__ __forceinline__ void softmax(int kb, uint64_t there) {
     if (kb + B > t.full || there != ~0ull) mask(kb, there);
     float top = s[0][0];
 #pragma unroll
     for (int e = 1; e < 16 * NS; ++e) top = fmaxf(top, s[e / 16][e % 16]);
-    top = max_x32(top) * p.scale2;
+    top = __builtin_fmaf(max_x32(top), p.scale2, -Half<T>::kLift);
     if (__any(top > m + kSlack)) {
       const float to = fmaxf(m, top), by = m == to ? 1.0f : exp2_fast(m - to);
       l *= by;

@@ -7,7 +7,7 @@ import pytest
 
 import sparse_weight_only_amd as sg
 from gpu_util import say
-from test_gpu_decode import F16, Setup, host, ints
+from test_gpu_decode import A, BF16, E, F16, U, Setup, host, ints
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -86,3 +86,51 @@ def test_candidates_below_slot_zero_see_nothing(n, ctx):
     for q in range(len(n)):
         a = int(s.new_start[q])
         assert (host(out)[a: a + max(0, n[q] - ctx[q])] == 0).all(), "a token without a slot saw a key"
+
+
+# ------------------------------------- weights far below the largest
+
+# what, dim, new tokens, slots, expected max, the plan's (tile rows, parts), strong keys: one in each wave's walk
+# (few rows: waves take 32-key blocks in turn; halves: each half of the first block of a part)
+FAR = [
+    ("few", 64, 1, 1 << 20, 1, (16, 1), [32 * w for w in range(8)]),
+    ("few", 256, 1, 1 << 19, 1, (16, 1), [32 * w for w in range(4)]),
+    ("halves", 64, 100, 1 << 20, 1025, (128, 4), [(p << 18) + 32 * h for p in range(4) for h in range(2)]),
+    ("many", 128, 200, 1 << 17, 1, (256, 1), [0]),
+    ("many", 256, 200, 1 << 17, 1, (256, 1), [0]),
+]
+
+
+@pytest.mark.parametrize("case", FAR, ids=lambda c: f"{c[0]}_d{c[1]}")
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("below", [14.0, 23.3, 24.9, 25.1, 31.0])
+def test_many_small_weights_beside_a_large_one(case, dtype, below):
+    """Keys `below` powers of two under the few strong ones add up over a long
+    context. V is 0 at the strong keys and 1 at the others, so that the result
+    is the others' share, A. Off by 3 u A, the scores' 2 D e S A, sums over n
+    keys 2 n e A; in FP16 each weight by half a subnormal of 2^-24 relative to
+    a largest weight of 2^7 at least, n 2^-32 of the strong ones' share; the
+    result's own half subnormal."""
+    what, dim, new, slots, max_ctx, plan, strong = case
+    say("case small weights", case, dtype, below)
+    page = 4096
+    k = torch.zeros(slots // page, page, 1, dim, dtype=dtype, device="cuda")
+    v = torch.ones_like(k)
+    k[..., 0] = -1.0
+    for t in strong:
+        k[t // page, t % page], v[t // page, t % page] = 0.0, 0.0
+    cache = sg.PagedCache.from_tensors(k, v)
+    seqs = sg.Sequences(ints([0, new]), ints([slots]), torch.arange(slots // page, dtype=torch.int32, device="cuda").reshape(1, -1))
+    q = torch.zeros(new, 1, dim, dtype=dtype, device="cuda")
+    q[..., 0] = 1.0
+    scale = float(np.float32(below * np.log(2.0)))
+    pl = cache.plan(seqs, new, 1, max_ctx)
+    assert (pl.tile_rows, pl.splits) == plan, "the case has left its path"
+    got = host(cache.attend(seqs, q, scale=scale, max_ctx=max_ctx))
+    n = slots - new + 1 + np.arange(new, dtype=np.float64)[:, None, None]
+    rest = (n - len(strong)) * np.exp(-scale)
+    ref = rest / (rest + len(strong))
+    tol = ref * (3 * U[dtype] + 2 * dim * E * scale + 2 * n * E)
+    if dtype == F16:
+        tol = tol + n * 2.0 ** -32 + A[F16]
+    assert (np.abs(got - ref) <= tol).all(), f"off by {np.abs(got - ref).max():.3e} of {ref.max():.3e}, allowed {tol.max():.3e}"
