@@ -134,3 +134,132 @@ def test_many_small_weights_beside_a_large_one(case, dtype, below):
     if dtype == F16:
         tol = tol + n * 2.0 ** -32 + A[F16]
     assert (np.abs(got - ref) <= tol).all(), f"off by {np.abs(got - ref).max():.3e} of {ref.max():.3e}, allowed {tol.max():.3e}"
+
+
+# --------------------------------------------- every slot by itself
+
+# n, ctx, heads, kv, dim, max_ctx, tile rows, more than one part
+NEEDLE = [
+    ([1], [3001], 4, 4, 128, 0, 16, True),
+    ([1], [3001], 4, 2, 256, 0, 16, True),
+    ([3], [801], 4, 4, 64, 1, 16, False),
+    ([30], [2777], 4, 2, 128, 0, 128, True),
+    ([30], [2777], 8, 4, 64, 0, 128, True),
+    ([130], [2310], 4, 4, 128, 0, 256, True),
+    ([130], [2310], 4, 2, 256, 0, 256, True),
+    ([150], [777], 4, 4, 80, 1, 256, False),
+]
+
+
+@pytest.mark.parametrize("case", NEEDLE, ids=lambda c: f"n{c[0][0]}_c{c[1][0]}_d{c[4]}_t{c[6]}")
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_every_kind_of_slot_counts_once(case, dtype):
+    """q = 0, so that a row's n visible keys weigh the same, and V is 0 except
+    in one slot a cache head: what comes out is its value / n (the powers of
+    two and their sums are exact; a reciprocal and a product in FP32, one
+    rounding), for first and last slots of blocks, parts, pages and the
+    context. A slot that is lost, counted twice or seen too early shows whole."""
+    n, ctx, heads, kv, dim, max_ctx, tile, split = case
+    say("case needle", case, dtype)
+    s = Setup(n, ctx, 8, heads, kv, dim, dtype, 34)
+    s.q.zero_()
+    new, all_ = n[0], ctx[0]
+    pl = s.cache.plan(s.seqs, new, heads, max_ctx)
+    assert pl.tile_rows == tile and (pl.splits > 1) == split, "the case has left its path"
+    blocks = -(-all_ // pl.block_keys)
+    per = -(-blocks // pl.splits) * pl.block_keys
+    marks = {0, 1, 3, 4, 7, 8, 15, 16, 31, 32, 33, 47, 48, 63, 64, 65, 95, 96, 127, 128, 255, 256, all_ // 2,
+             all_ - new - 1, all_ - new, all_ - new // 2 - 1, all_ - 2, all_ - 1, all_ // pl.block_keys * pl.block_keys}
+    marks |= {p * per + d for p in range(1, pl.splits) for d in (-1, 0, 32)}
+    marks |= {m - 1 for m in (all_ // 8 * 8, all_ // 32 * 32, all_ // 64 * 64)}
+    marks = sorted(m for m in marks if 0 <= m < all_)
+    marks += marks[: -len(marks) % kv]
+    value = 1000.0 + 8.0 * np.arange(dim)               # below 2^12, multiples of 8: exact in FP16
+    if dtype == BF16:
+        value = 1024.0 + 16.0 * (np.arange(dim) % 64)   # eight bits
+    seen = all_ - new + 1 + np.arange(new, dtype=np.float64)
+    flat = torch.from_numpy(s.pages[0].astype(np.int64)).cuda()
+    hv = torch.tensor(value, device="cuda").to(dtype)
+    assert np.array_equal(host(hv), value)
+    for i in range(0, len(marks), kv):
+        s.vc.zero_()
+        at = marks[i: i + kv]
+        for h, t in enumerate(at):
+            s.vc[flat[t // 8], t % 8, h] = hv
+        got = host(s.cache.attend(s.seqs, s.q, max_ctx=max_ctx))
+        there = np.array([at[h // (heads // kv)] for h in range(heads)])[None, :] < seen[:, None]
+        ref = there[:, :, None] * value / seen[:, None, None]
+        assert (np.abs(got - ref) <= ref * (U[dtype] + 3 * E)).all(), f"slots {at}"
+
+
+# ------------------------------------------------ the joins' later turns
+
+JOIN = [
+    # n, ctx, heads, kv, dim, dtype, parts
+    ([128, 20], [4096, 700], 8, 1, 128, F16, 16),
+    ([128, 20], [4096, 700], 8, 1, 128, BF16, 16),
+    ([64, 64], [3000, 2304], 8, 1, 64, F16, 11),
+    ([64, 64], [3000, 2304], 8, 1, 64, BF16, 11),
+    ([100, 30], [2600, 300], 8, 1, 256, F16, 10),
+    ([100, 30], [2600, 300], 8, 1, 256, BF16, 10),
+    ([130], [2800], 8, 2, 184, F16, 10),
+]
+
+
+@pytest.mark.parametrize("case", JOIN, ids=lambda c: f"n{c[0][0]}_c{c[1][0]}_d{c[4]}_{str(c[5])[6:]}")
+def test_join_of_many_rows_and_many_parts(case):
+    """More than 1024 rows in more than eight parts, the largest scores behind
+    the eighth, and a sequence with fewer parts beside it."""
+    n, ctx, heads, kv, dim, dtype, parts = case
+    say("case join", case)
+    s = Setup(n, ctx, 16, heads, kv, dim, dtype, 35)
+    pl = s.cache.plan(s.seqs, s.tokens, heads)
+    assert s.tokens * heads >= 1024 and pl.splits == parts > 8, "the case has left its path"
+    blocks = -(-ctx[0] // pl.block_keys)
+    late = 8 * -(-blocks // parts) * pl.block_keys
+    assert late < ctx[0] - 2 * 16
+    for p in s.pages[0, late // 16 + 1:]:
+        s.kc[int(p)] *= 2.0
+    out = s.cache.attend(s.seqs, s.q)
+    s.check(out, s.want(), "join")
+    assert torch.equal(out, s.cache.attend(s.seqs, s.q)), "not the same bits twice"
+
+
+# ------------------------------------------------------ many sequences
+
+MANY_SEQS = [
+    # n, ctx, heads, kv, dim, dtype, tile rows, parts
+    ([1] * 70, [1 + 7 * i % 300 for i in range(70)], 4, 2, 64, F16, 16, 1),
+    ([1, 0, 2] * 43 + [1], [5 + 11 * i % 200 for i in range(130)], 2, 1, 128, BF16, 16, 1),
+    ([1] * 69 + [3], [2 + i for i in range(69)] + [2000], 2, 1, 128, F16, 16, 3),
+    ([3, 0] * 40, [3 + i for i in range(79)] + [1600], 16, 1, 64, BF16, 128, 6),
+    ([100, 0] * 40 + [9], [101 + i % 50 for i in range(80)] + [1300], 2, 1, 72, F16, 128, 3),
+    ([300, 0] * 33, [300 + i % 20 for i in range(66)], 1, 1, 128, F16, 256, 1),
+]
+
+
+@pytest.mark.parametrize("case", MANY_SEQS, ids=lambda c: f"s{len(c[0])}_t{c[6]}_p{c[7]}")
+def test_more_than_64_sequences(case):
+    n, ctx, heads, kv, dim, dtype, tile, parts = case
+    say("case many sequences", len(n), case[2:])
+    s = Setup(n, ctx, 16, heads, kv, dim, dtype, 36, 1, 2)
+    pl = s.cache.plan(s.seqs, s.tokens, heads)
+    assert len(n) > 64 and (pl.tile_rows, pl.splits) == (tile, parts), "the case has left its path"
+    out = torch.full_like(s.q, 55.0)
+    s.cache.attend(s.seqs, s.q, out=out)
+    want = s.want()
+    s.check(out, want, "many sequences")
+    assert (host(out)[np.isnan(want[0][:, 0, 0])] == 55.0).all(), "a row of no sequence was written"
+
+
+# --------------------------------------------------------- head widths
+
+@pytest.mark.parametrize("dim", [104, 120, 136, 160, 192, 216, 248])
+@pytest.mark.parametrize("n,ctx,tile", [([1, 2], [900, 33], 16), ([150], [260], 256), ([20], [1200], 0)])
+def test_head_widths_between(dim, n, ctx, tile):
+    say("case width", dim, n, ctx)
+    dtype = BF16 if dim % 16 else F16
+    s = Setup(n, ctx, 8, 3, 1, dim, dtype, 37, head_major=dim > 200)
+    tile = tile or (128 if dim <= 128 else 256)
+    assert s.cache.plan(s.seqs, s.tokens, 3).tile_rows == tile, "the case has left its path"
+    s.check(s.cache.attend(s.seqs, s.q), s.want(), f"{dim} columns")
