@@ -7,7 +7,8 @@ import pytest
 
 import sparse_weight_only_amd as sg
 from gpu_util import say
-from test_gpu_decode import A, BF16, E, F16, U, Setup, host, ints
+from oracle import decode as odec
+from test_gpu_decode import A, BF16, E, F16, F32, U, Setup, host, ints
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -263,3 +264,26 @@ def test_head_widths_between(dim, n, ctx, tile):
     tile = tile or (128 if dim <= 128 else 256)
     assert s.cache.plan(s.seqs, s.tokens, 3).tile_rows == tile, "the case has left its path"
     s.check(s.cache.attend(s.seqs, s.q), s.want(), f"{dim} columns")
+
+
+# --------------------------------------------------------- bias lists
+
+@pytest.mark.parametrize("n", [255, 300, 511, 512, 513])
+@pytest.mark.parametrize("spread", [200, 4096, 9001])
+@pytest.mark.parametrize("history", [False, True])
+def test_bias_lists_around_the_limits(n, spread, history):
+    """Lists that the lanes hold and that they do not, more entries in one part
+    than the lanes go through and fewer, copies among them; every step is exact."""
+    say("case bias limits", n, spread, history)
+    rng = np.random.default_rng(n + spread)
+    ids, vals = rng.integers(0, spread, (2, n)), rng.integers(-50, 50, (2, n)) * 0.25
+    x = torch.randint(-9, 9, (2, 9001), device="cuda").float()
+    args = dict(bias_ids=ints(ids.ravel()), bias_start=ints([0, n, 2 * n]), bias_values=torch.tensor(vals.ravel(), dtype=F32, device="cuda"))
+    want = dict(bias=[list(zip(i, v)) for i, v in zip(ids, vals)])
+    if history:
+        h, two = [[3, 3, 5], list(range(50))], torch.full((2,), 2.0, device="cuda")
+        args.update(history=ints(h[0] + h[1]), history_start=ints([0, 3, 53]), repetition=two, presence=two)
+        want.update(history=h, repetition=[2.0] * 2, presence=[2.0] * 2)
+    ref = odec.adjust_logits(host(x), **want)
+    assert np.array_equal(host(sg.adjust_logits(x, **args)), ref)
+    assert np.array_equal(host(sg.adjust_logits(x, out=x, **args)), ref)
