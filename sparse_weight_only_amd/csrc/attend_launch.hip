@@ -51,7 +51,9 @@ int make_shape(const sgemv_cache* c, const sgemv_seqs* s, int32_t tokens, int32_
   // only add to what is joined (131071 slots, 8 heads: 100 us with 256, 102
   // with 512, 107 with 1024). A part has two blocks at least in the few-row
   // kernel (700 slots, 32 heads: 10.0 us with parts of 64, 11.0 of 128, 12.8
-  // of 256), four in the other.
+  // of 256), four in the other (8 heads, 27 rows over 1500 slots: 15.4 us with
+  // parts of 256, 14.0 of 128, 22.2 of 512; 300 rows over 2000: 27.9, 28.3 and
+  // 32.1; 64 tokens of 32 heads sharing 8 over 4000: 30.4, 28.9 and 32.2).
   const int64_t want = (!h.few && h.dp == 64 ? 2 : 1) * kCus / (tiles * c->heads);
   const int64_t most = ctx / (h.few ? 64 : 256);
   int64_t splits = want < most ? want : most;
@@ -159,7 +161,8 @@ extern "C" int sgemv_attend(const sgemv_cache* cache, const sgemv_seqs* seqs, co
   if (h.splits > 1) {
     const int64_t rows = (int64_t)q->tokens * q->heads;
     // a workgroup a row while that fills the chip a few times over at most,
-    // then DP/4 lanes a row
+    // then DP/4 lanes a row (128 rows of 31 parts: 9.8 us of both kernels, 12.8
+    // the other way; 1024 of 15: 23.3 and 23.4; 4096 of 16: 40.8 and 37.8)
     const bool many = rows >= 4 * kCus;
     const int64_t grid = many ? (rows * (h.dp / 4) + sgemv_dev::kJoinLanes - 1) / sgemv_dev::kJoinLanes : rows;
     hipLaunchKernelGGL(sgemv_dev::get_attend_join(bf16, p.dim, many), dim3((uint32_t)grid), dim3(sgemv_dev::kJoinLanes), 0,

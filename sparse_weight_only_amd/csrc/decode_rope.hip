@@ -145,7 +145,9 @@ int launch(RopeParams& p, int tokens, int dim, int dtype, void* stream) {
   p.per_pass = kLanes / p.chunks;
   const int all = (p.nq + 2 * p.nkv + p.per_pass - 1) / p.per_pass;
   // few tokens: a workgroup for each pass, for the latency of one; many: one
-  // workgroup a token, so that its sines are computed once
+  // workgroup a token, so that its sines are computed once (32 heads of q, k and
+  // v; as many workgroups as there are passes, or one a token: 16 tokens 4.4 and
+  // 10.3 us, 512 tokens 10.7 and 12.6, 9.6 in between, 4096 tokens 59 and 44)
   int groups = all;
   while (groups > 1 && (int64_t)groups * tokens > 2048) groups = (groups + 1) / 2;
   p.passes = (all + groups - 1) / groups;
