@@ -429,7 +429,8 @@ typedef struct sgemv_rope_t {
  * fast pairs stay and slow ones are divided.
  *   turns_out : host double[rot_dim / 2].
  * Errors: EINVAL (rot_dim odd or outside 2..256; base <= 0, factor <= 0,
- * context < 0, high <= low with a context, anything not finite; NULL). */
+ * context < 0, high <= low with a context; anything not finite, frequencies
+ * and high - low included; NULL). */
 int sgemv_rope_table(int32_t rot_dim, double base, double factor, double context, double low, double high,
                      double* turns_out);
 

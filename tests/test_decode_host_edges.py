@@ -9,6 +9,7 @@ import pytest
 import sparse_weight_only_amd as sg
 from oracle import decode as odec
 from sparse_weight_only_amd import _build
+from sparse_weight_only_amd.sgemv import SGEMV_EINVAL
 
 torch = pytest.importorskip("torch")
 
@@ -42,3 +43,17 @@ def test_visible_keys_under_sanitizers():
         _build_san.build_index_check()
     r = subprocess.run([exe], stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.startswith("ok"), r.stdout[-3000:]
+
+
+@pytest.mark.parametrize("args", [(128, 1e-320), (8, 1e-300, 1e-300), (8, 1e4, 2.0, 1e3, -1e308, 1e308), (64, 1e-320, 1.0, 10.0)])
+def test_rope_table_refuses_frequencies_that_are_not_finite(args):
+    """Finite arguments whose powers, quotients or differences overflow: every angle would be NaN."""
+    with pytest.raises(sg.SgemvError) as e:
+        sg.rope_table(*args)
+    assert e.value.code == SGEMV_EINVAL
+
+
+@pytest.mark.parametrize("args", [(8, 1e-300), (256, 1e300), (8, 1e4, 1e300), (8, 1e4, 2.0, 1e300)])
+def test_rope_table_takes_extreme_arguments(args):
+    got = sg.rope_table(*args)
+    assert np.isfinite(got).all() and np.all(got >= 0)
