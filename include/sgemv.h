@@ -493,7 +493,8 @@ int sgemv_attend_plan(const sgemv_cache* cache, const sgemv_seqs* seqs, int32_t 
  *                says, 16-byte aligned (NULL where that is 0); not shared by
  *                calls that may run at the same time. What it holds before
  *                does not matter.
- * A token that sees nothing gets zeros. A slot that a token does not see has
+ * A token that sees nothing gets zeros (as it does where all scores are
+ * -inf, from infinite keys). A slot that a token does not see has
  * no part in its result, whatever it holds (infinities and NaN included), and
  * so have slots behind a sequence's end.
  * Numerics: scores, the running maximum, sums and outputs in FP32; each p_t

@@ -170,6 +170,9 @@ struct Few {
     float s[8];
     scores(kb, b, s);
     const float base = m == -__builtin_inff() ? 0.0f : m;
+    // a key that is seen may have a score of -inf too
+    const int row = t.row0 + r < t.rows ? t.row0 + r : t.rows - 1;
+    const uint32_t bits = visible_bits(p, t, row / p.group, kb) & b.there;
     for (int key = 0; key < kFewBlock; ++key) {
       // the lane that holds this key's score for row r
       const int from = r + 16 * (key / 4 % 4), e = key % 4;
@@ -178,8 +181,8 @@ struct Few {
       const float sk = __shfl(key < 16 ? s0 : s1, from);
       if (!(b.there >> key & 1u)) continue;
       const int page = t.pages[(kb + key) >> p.seq.page_shift];
-      const uint16_t* row = vh + element(page, p.v_page, (kb + key) & ((1 << p.seq.page_shift) - 1), p.v_slot);
-      if (sk == -__builtin_inff()) continue;
+      const uint16_t* vr = vh + element(page, p.v_page, (kb + key) & ((1 << p.seq.page_shift) - 1), p.v_slot);
+      if (!(bits >> key & 1u)) continue;
       const float pk = exp2_fast(__builtin_fmaf(sk, p.scale2, -base));
 #pragma unroll
       for (int e4 = 0; e4 < 4; ++e4) {
@@ -187,7 +190,7 @@ struct Few {
         for (int u = 0; u < VD; ++u) {
           const int d = (4 * g + e4) * VC + 2 * u;
           if (d >= p.dim) continue;
-          const uint32_t w = load<uint32_t>(addr(row + d));
+          const uint32_t w = load<uint32_t>(addr(vr + d));
           o[2 * u][e4] += pk * Half<T>::lo(w);
           o[2 * u + 1][e4] += pk * Half<T>::hi(w);
         }

@@ -89,6 +89,33 @@ def test_candidates_below_slot_zero_see_nothing(n, ctx):
         assert (host(out)[a: a + max(0, n[q] - ctx[q])] == 0).all(), "a token without a slot saw a key"
 
 
+# ------------------------------------------------- infinite keys
+
+@pytest.mark.parametrize("n,ctx", [([1], [200]), ([3], [90]), ([90], [1200]), ([300], [400])])
+def test_keys_of_minus_infinity(n, ctx):
+    """A score of -inf is a weight of 0 like any other: it leaves the others as
+    they are, and times an infinite value it is no number, in every kernel."""
+    say("case infinite keys", n)
+    s = Setup(n, ctx, 16, 2, 1, 64, F16, 38)
+    s.q[..., 7] = s.q[..., 7].abs() + 0.5
+    slot = ctx[0] - n[0] // 2 - 1
+    at = int(s.pages[0, slot // 16]), slot % 16
+    s.kc[at[0], at[1], 0, 7] = float("-inf")
+    with np.errstate(invalid="ignore"):
+        want = s.want()
+    worst = want[2]
+    worst[~np.isfinite(worst)] = 64 * 5.0 * 5.0 * 64 ** -0.5   # of the finite scores: at most this
+    got = s.cache.attend(s.seqs, s.q)
+    s.check(got, want, "-inf")
+    s.vc[at[0], at[1], 0, 5] = float("inf")
+    got = host(s.cache.attend(s.seqs, s.q))
+    sees = np.arange(ctx[0] - n[0], ctx[0]) >= slot
+    assert np.isnan(got[sees][:, :, 5]).all() and np.isfinite(got[~sees]).all() and np.isfinite(np.delete(got, 5, 2)).all()
+    s.kc[..., 7] = float("-inf")
+    s.vc[at[0], at[1], 0, 5] = 0.0
+    assert (host(s.cache.attend(s.seqs, s.q)) == 0).all(), "all scores are -inf"
+
+
 # ------------------------------------- weights far below the largest
 
 # what, dim, new tokens, slots, expected max, the plan's (tile rows, parts), strong keys: one in each wave's walk
