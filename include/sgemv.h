@@ -472,6 +472,9 @@ typedef struct sgemv_attend_plan_t {
  *   max_ctx : the longest sequence the caller expects, or 0 for what
  *             pages_per_seq pages hold. It shapes the launch only: longer
  *             sequences are computed just as well.
+ * All sequences get the same number of parts, and the kernel for the average
+ * number of rows: one that is many times longer than the others, in context or
+ * in new tokens, is faster in a call of its own.
  * Errors: EINVAL, EALIGN, ESIZE. */
 int sgemv_attend_plan(const sgemv_cache* cache, const sgemv_seqs* seqs, int32_t tokens, int32_t heads, int32_t max_ctx,
                       sgemv_attend_plan_t* out);
