@@ -513,6 +513,71 @@ int sgemv_attend(const sgemv_cache* cache, const sgemv_seqs* seqs, const sgemv_r
                  const uint32_t* tree_dev, int32_t tree_words, int32_t max_ctx, void* workspace_dev, int64_t workspace_bytes,
                  void* hip_stream);
 
+/* sgemv_attend_window - sgemv_attend through a sliding window: a token at slot
+ * a sees slot t <= a where t > a - window (itself and the window - 1 before it)
+ * or t < sinks (the first tokens of its sequence stay visible).
+ *   window : >= 1; 0 for none, as sgemv_attend (sinks must be 0 then).
+ *   sinks  : >= 0.
+ * With a tree a token sees new tokens by its bits alone, however many, and the
+ * m of its sequence that it sees so come off its window: it sees a slot before
+ * the new tokens where that is one of the last window - m or of the first
+ * `sinks`. Blocks of keys that no row of a tile sees are not read, so pages out
+ * of every token's window may be given back (their entries may hold anything).
+ * All else as sgemv_attend, the numerics too; its plan is
+ * sgemv_attend_window_plan's. Errors: as sgemv_attend, and EINVAL (window or
+ * sinks below 0, sinks without a window). */
+int sgemv_attend_window_plan(const sgemv_cache* cache, const sgemv_seqs* seqs, int32_t tokens, int32_t heads, int32_t window,
+                             int32_t sinks, int32_t max_ctx, sgemv_attend_plan_t* out);
+int sgemv_attend_window(const sgemv_cache* cache, const sgemv_seqs* seqs, const sgemv_rows* q, const sgemv_rows* out, float scale,
+                        const uint32_t* tree_dev, int32_t tree_words, int32_t window, int32_t sinks, int32_t max_ctx,
+                        void* workspace_dev, int64_t workspace_bytes, void* hip_stream);
+
+/* A paged cache in 8 bits: K and V as e4m3 codes (OCP: 4 significant bits, up
+ * to 448, no infinities), times a power of two that a block of scale_slots
+ * slots shares for each head, K's and V's apart. Code (page, slot, head,
+ * column) of K is k[page * k_page + slot * k_slot + head * k_head + column];
+ * scales[((page * (page_size / scale_slots) + slot / scale_slots) * heads +
+ * head) * 2 + (0 for K, 1 for V)] holds e for a scale of 2^(e - 127) (the E8M0
+ * type; 255, which that type has for a NaN, counts as 2^128 here).
+ * k and v 16-byte aligned, scales 2; strides in bytes, multiples of 16; columns
+ * contiguous. head_dim: a multiple of 16 up to 256. page_size as sgemv_cache;
+ * scale_slots: a power of two, 8..128, at most page_size. Queries, new keys
+ * and values and results are FP16 or BF16, as a call's rows say. */
+typedef struct sgemv_cache8 {
+  void *k, *v;
+  uint8_t* scales;
+  int64_t k_page, k_slot, k_head;
+  int64_t v_page, v_slot, v_head;
+  int32_t pages, page_size, heads, head_dim, scale_slots;
+} sgemv_cache8;
+
+/* sgemv_append8 - sgemv_append into a cache in 8 bits. Of a block, a head and
+ * one of K and V let A be the largest finite magnitude among its new values (k
+ * turned, in FP32) and e(A) the least exponent with A <= 448 2^e, from -96 to
+ * 120. The block's exponent becomes e(A) where its first slot is new, and the
+ * larger of e(A) and what it was where it holds older tokens, whose codes
+ * are rounded once more if it grew (which changes those below 2^-6 times the new
+ * scale only). New values are rounded to codes once; what is not finite becomes
+ * the NaN code. Slots behind the last new token stay as they are.
+ * A block of scale_slots slots that gets new tokens is one sequence's alone.
+ * q_out as in sgemv_append, and positions, errors and the rest. */
+int sgemv_append8(const sgemv_cache8* cache, const sgemv_seqs* seqs, const sgemv_rope_t* rope, const int32_t* positions_dev,
+                  const sgemv_rows* q, const sgemv_rows* q_out, const sgemv_rows* k, const sgemv_rows* v, void* hip_stream);
+
+/* sgemv_attend8 - sgemv_attend_window (window 0: sgemv_attend) over a cache in
+ * 8 bits: attention over the values that its codes and scales stand for.
+ * A slot that a token does not see has no part in its result, whatever its code
+ * holds; nor have the scales of blocks without a slot of the sequence, or
+ * without one that a token of it can see.
+ * Numerics: codes are exact in the queries' type; each p_t is rounded to it as in
+ * sgemv_attend, so |out - exact| is within the bound given there. In BF16 values
+ * in blocks of exponents up to -96 may count as 0 beside others. */
+int sgemv_attend8_plan(const sgemv_cache8* cache, const sgemv_seqs* seqs, int32_t tokens, int32_t heads, int32_t window, int32_t sinks,
+                       int32_t max_ctx, sgemv_attend_plan_t* out);
+int sgemv_attend8(const sgemv_cache8* cache, const sgemv_seqs* seqs, const sgemv_rows* q, const sgemv_rows* out, float scale,
+                  const uint32_t* tree_dev, int32_t tree_words, int32_t window, int32_t sinks, int32_t max_ctx, void* workspace_dev,
+                  int64_t workspace_bytes, void* hip_stream);
+
 /* Penalties, biases and masks on rows of logits; all pointers are device
  * memory. x and out: `rows` rows of `vocab` values, element aligned, strides
  * in elements. out_dtype: dtype, or SGEMV_F32. out may be x (same type and
@@ -551,6 +616,37 @@ typedef struct sgemv_logits {
  * synchronising; the same bits on every call.
  * Errors: EINVAL, EALIGN, ESIZE (over 65535 rows), EHIP. */
 int sgemv_adjust_logits(const sgemv_logits* g, void* hip_stream);
+
+/* The choice of a token for each row of logits; all pointers are device
+ * memory. x: `rows` rows of `vocab` values, element aligned, stride in
+ * elements. The per-row arrays may change between replays. */
+typedef struct sgemv_sampling {
+  const void* x;
+  int64_t x_stride;
+  const float* uniform;        /* [rows] random numbers, each in [0, 1)                            */
+  const float* temperature;    /* [rows] each; NULL: 1. 0 or less, or NaN: the largest logit      */
+  const int32_t* top_k;        /* [rows] how many of the largest; NULL, 0 or less: all             */
+  const float* top_p;          /* [rows] NULL, 1 or more, NaN: all                                 */
+  const float* min_p;          /* [rows] NULL, 0 or less, NaN: all                                 */
+  int32_t* ids;                /* [rows] out                                                       */
+  float* logprob;              /* [rows] out, or NULL                                              */
+  int32_t rows, vocab, dtype;
+} sgemv_sampling;
+
+/* sgemv_sample - with p_v = exp((x_v - max x) / temperature), a row keeps the
+ * tokens of p_v >= min_p, of those the top_k largest, and of those the fewest
+ * largest whose sum reaches top_p of theirs (one at least); of equal logits
+ * lower ids count as larger. The token is the first id, by id, up to which the
+ * kept p sum to more than uniform times their sum, so equal uniform numbers
+ * give equal tokens. logprob: ln of its share of that sum. NaN and -inf are
+ * never chosen; where a row has nothing else its token is -1 and logprob -inf.
+ * Logits of +inf share the row alone. uniform outside [0, 1) counts as 0 or as
+ * the largest number below 1.
+ * Numerics: exponents and exponentials in 64 bits, p in whole multiples of
+ * 2^-43 and so summed exactly, in any order: the same tokens on every call.
+ * Enqueues one kernel and returns without synchronising.
+ * Errors: EINVAL, EALIGN, ESIZE (vocab over 2^20, over 65535 rows), EHIP. */
+int sgemv_sample(const sgemv_sampling* s, void* hip_stream);
 
 /* sgemv_strerror - static description of a status code (never NULL). */
 const char* sgemv_strerror(int code);

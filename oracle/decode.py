@@ -1,9 +1,10 @@
 """FP64 definitions of the operators between the GEMVs of a decode step.
 
 Each is written per token or per row, in the order of its definition, with
-plain loops: rotary positions, the append to a paged cache, attention over
-it, and penalties, biases and masks on logits. ``attend`` also returns the
-mean absolute value that its error bound is relative to.
+plain loops: rotary positions, the append to a paged cache (of the values'
+own type, or in 8 bits), attention over it, penalties, biases and masks on
+logits, and the choice of tokens. ``attend`` also returns the mean absolute
+value that its error bound is relative to.
 """
 from __future__ import annotations
 
@@ -61,7 +62,73 @@ def append(k_cache, v_cache, k, v, new_start, ctx_len, pages):
     return kc, vc
 
 
-def attend(q, k_cache, v_cache, new_start, ctx_len, pages, scale, tree=None):
+# The values of e4m3's codes 0..126 (127 is NaN): sign apart, 4 exponent and 3
+# mantissa bits, subnormals in steps of 2^-9.
+E4M3 = np.array([(m / 8 * 2.0 ** -6 if e == 0 else (1 + m / 8) * 2.0 ** (e - 7)) for e in range(16) for m in range(8)][:127])
+
+
+def to_e4m3(x):
+    """Codes of FP64 values up to 448 in magnitude, to the nearest, ties to the even code; what is not finite: 0x7f."""
+    x = np.asarray(x, np.float64)
+    a = np.where(np.isfinite(x), np.abs(x), 0.0)
+    assert a.max(initial=0.0) <= 448.0
+    lo = np.clip(np.searchsorted(E4M3, a, side="right") - 1, 0, 125)
+    mid = (E4M3[lo] + E4M3[lo + 1]) / 2
+    code = np.where(a > mid, lo + 1, np.where(a < mid, lo, lo + lo % 2))
+    return np.where(np.isfinite(x), code | np.where(np.signbit(x), 128, 0), 0x7F).astype(np.uint8)
+
+
+def of_e4m3(codes):
+    codes = np.asarray(codes)
+    v = np.append(E4M3, np.nan)[codes & 127]
+    return np.where(codes & 128, -v, v)
+
+
+def values8(codes, scales, which):
+    """FP64 values of codes [pages, page, H, D] with scale bytes [pages, blocks, H, 2]; which: 0 for K, 1 for V."""
+    each = codes.shape[1] // scales.shape[1]
+    return of_e4m3(codes) * 2.0 ** (np.repeat(scales[..., which].astype(int), each, 1) - 127)[..., None]
+
+
+def exponent8(a):
+    """The least e from -96 to 120 with a <= 448 2^e."""
+    e = -96
+    while a > 448.0 * 2.0 ** e and e < 120:
+        e += 1
+    return e
+
+
+def append8(codes, scales, x, which, new_start, ctx_len, pages):
+    """Rows x [T, H, D] (FP64, k turned) into copies of codes [pages, page, H, D] and scale bytes [pages, blocks, H, 2]."""
+    codes, scales = codes.copy(), scales.copy()
+    n_pages, page, H, _ = codes.shape
+    each = page // scales.shape[1]
+    rows = {}                                                   # block -> its new rows
+    for row, (s, i, slot) in slots(new_start, ctx_len).items():
+        if 0 <= slot < page * pages.shape[1] and 0 <= int(pages[s, slot // page]) < n_pages:
+            rows.setdefault((int(pages[s, slot // page]), slot % page // each), []).append((slot % page % each, row))
+    for (at, blk), new in rows.items():
+        first = min(new)[0]
+        for h in range(H):
+            y = np.stack([x[row, h] for _, row in new])
+            e = exponent8(np.abs(y[np.isfinite(y)]).max(initial=0.0))
+            if first > 0:
+                was = int(scales[at, blk, h, which]) - 127
+                e = max(e, was)
+                old = slice(blk * each, blk * each + first)
+                codes[at, old, h] = to_e4m3_keeping_nan(codes[at, old, h], was - e)
+            scales[at, blk, h, which] = e + 127
+            for r, row in new:
+                codes[at, blk * each + r, h] = to_e4m3(x[row, h] * 2.0 ** -e)
+    return codes, scales
+
+
+def to_e4m3_keeping_nan(codes, by):
+    """Codes times 2^by (by <= 0), rounded; a NaN stays as it is."""
+    return codes if by == 0 else np.where(codes & 127 == 127, codes, to_e4m3(np.nan_to_num(of_e4m3(codes)) * 2.0 ** by))
+
+
+def attend(q, k_cache, v_cache, new_start, ctx_len, pages, scale, tree=None, window=0, sinks=0):
     """(out, mean, worst, keys): FP64 attention [T, Hq, D] (zeros where no key is
     visible, NaN for rows of no sequence), sum p |v| / sum p, the largest
     sum_d |q_d k_d| scale of each (row, head), and its number of visible keys."""
@@ -73,7 +140,12 @@ def attend(q, k_cache, v_cache, new_start, ctx_len, pages, scale, tree=None):
         ctx = min(int(ctx_len[s]), pages.shape[1] * page)
         old = ctx - (int(new_start[s + 1]) - int(new_start[s]))
         see = []
+        low = old + i + 1 - window                  # the first slot that a window leaves, the sinks apart
+        if tree is not None:
+            low = min(old, old - window + sum(int(tree[row, j // 32]) >> (j % 32) & 1 for j in range(min(ctx - old, 32 * tree.shape[1]))))
         for t in range(ctx):
+            if window and sinks <= t < low:
+                continue
             if not 0 <= int(pages[s, t // page]) < n_pages:
                 continue
             if tree is None:
@@ -124,3 +196,37 @@ def adjust_logits(x, history=None, prompt_len=None, repetition=None, frequency=N
         if masks is not None and masks[b] is not None:
             y[b, ~np.asarray(masks[b], bool)] = -np.inf
     return y
+
+
+def sample(x, uniform, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
+    """(token, ln of its share, the least distance of a border from where it would decide otherwise) of one row of logits, FP64."""
+    x = np.asarray(x, np.float64)
+    x = np.where(np.isnan(x), -np.inf, x)
+    if x.max(initial=-np.inf) == -np.inf:
+        return -1, -math.inf, math.inf
+    if not temperature > 0:
+        return int(x.argmax()), 0.0, math.inf
+    order = sorted((i for i in range(len(x)) if x[i] > -np.inf), key=lambda i: (-x[i], i))
+    with np.errstate(invalid="ignore"):
+        p = np.where(x == x.max(), 1.0, np.exp((x - x.max()) / temperature))
+    far = math.inf
+    if min_p > 0:
+        far = min([far] + [abs(p[i] - min(min_p, 1.0)) for i in order if p[i] != 1.0])
+        order = [i for i in order if p[i] >= min(min_p, 1.0)]
+    if top_k > 0:
+        order = order[:top_k]
+    if top_p < 1:
+        total, run = math.fsum(p[i] for i in order), 0.0
+        for n, i in enumerate(order):
+            run += p[i]
+            far = min(far, abs(run / total - top_p))
+            if run >= max(top_p, 0.0) * total:
+                break
+        order = order[: n + 1]
+    order.sort()
+    total = math.fsum(p[i] for i in order)
+    run = np.cumsum([p[i] for i in order]) / total
+    u = min(max(uniform, 0.0), 1.0 - 2.0 ** -53) if uniform == uniform else 0.0
+    at = min(int((run <= u).sum()), len(order) - 1)
+    far = min([far] + [abs(r - u) for r in run[:-1]])
+    return order[at], math.log(p[order[at]] / total), far

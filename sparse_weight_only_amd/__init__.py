@@ -12,5 +12,5 @@ from .sgemv import (  # noqa: F401
     LIST_MAX, run_list, plan_list, LIST_TABLE_MAX, ListLaunch, list_table, run_list_table,
 )
 from .decode import (  # noqa: F401
-    Rope, Sequences, PagedCache, adjust_logits, rope_table, AttendPlan,
+    Rope, Sequences, PagedCache, PagedCache8, adjust_logits, sample, rope_table, AttendPlan,
 )

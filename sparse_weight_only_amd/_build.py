@@ -17,7 +17,9 @@ LIB = os.path.join(OUT_DIR, "libsgemv.so")
 HOST_SRCS = ["host_pack.cpp", "host_layout.cpp", "host_rope.cpp"]
 HIP_SRCS = ["sgemv_k_nk1.hip", "sgemv_k_nk2.hip", "sgemv_k_nk4.hip", "sgemv_k_f16.hip", "sgemv_k_rb.hip", "sgemv_launch.hip",
             "sgemv_probe.hip", "sgemv_k_list.hip",
-            "decode_rope.hip", "attend_k_few.hip", "attend_k_many.hip", "attend_launch.hip", "decode_logits.hip"]
+            "attend_k_many8_window.hip", "attend_k_many8.hip", "attend_k_many_window.hip", "attend_k_many.hip",
+            "attend_k_few8_window.hip", "attend_k_few8.hip", "attend_k_few_window.hip", "attend_k_few.hip", "attend_k_join.hip",
+            "attend_launch.hip", "decode_rope.hip", "decode_append8.hip", "decode_logits.hip", "decode_sample.hip"]
 
 
 def _hipcc() -> str:

@@ -36,11 +36,13 @@ INDEX_SRC = os.path.join(_INDEX_DIR, "index_check.cpp")
 INDEX_CHECK = os.path.join(_INDEX_DIR, "_build", "index_check")
 VISIBLE_SRC = os.path.join(_INDEX_DIR, "visible_check.cpp")
 VISIBLE_CHECK = os.path.join(_INDEX_DIR, "_build", "visible_check")
+WINDOW_SRC = os.path.join(_INDEX_DIR, "window_check.cpp")
+WINDOW_CHECK = os.path.join(_INDEX_DIR, "_build", "window_check")
 
 
 def build_index_check(verbose: bool = False) -> str:
     os.makedirs(os.path.dirname(INDEX_CHECK), exist_ok=True)
-    for src, exe in ((INDEX_SRC, INDEX_CHECK), (VISIBLE_SRC, VISIBLE_CHECK)):
+    for src, exe in ((INDEX_SRC, INDEX_CHECK), (VISIBLE_SRC, VISIBLE_CHECK), (WINDOW_SRC, WINDOW_CHECK)):
         tmp = exe + ".tmp"
         _run(["g++", "-std=c++17", "-O1", "-g", "-fno-omit-frame-pointer", "-fsanitize=address,undefined",
               "-fno-sanitize-recover=all", "-Wall", "-Wextra", src, "-o", tmp], verbose)

@@ -38,6 +38,11 @@ struct AttendParams : TileView {
   int32_t slots;          // row tiles, empty ones included
   float scale2;           // scale * log2(e): scores in powers of two
   float* part;            // splits > 1: [row][split][dim] sums, then [row][split] of (m, sum of p)
+  // a cache in 8 bits: k and v are codes, one byte each, and of every block of
+  // 2^exp_shift slots and head there are the exponents (K's in the low byte, V's)
+  const uint16_t* exps;   // [page][block][head]
+  uint32_t exp_page;      // of them in a page
+  int32_t exp_shift;
 };
 typedef void (*AttendFn)(AttendParams);
 
@@ -47,7 +52,6 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 b16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 b16x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t dword2 __attribute__((ext_vector_type(2)));
 
 template <class T> struct Half;
 template <> struct Half<_Float16> {
@@ -81,6 +85,53 @@ template <> struct Half<__bf16> {
   static __device__ __forceinline__ float lo(uint32_t u) { return __builtin_bit_cast(float, u << 16); }
   static __device__ __forceinline__ float hi(uint32_t u) { return __builtin_bit_cast(float, u & 0xffff0000u); }
 };
+
+// A cache in 8 bits. Keys and values are e4m3 codes times powers of two that a
+// block of slots shares: e4m3 has 4 significant bits, so codes are exact in
+// either 16-bit type, and the conversion takes a power of two along for nothing.
+//   K: the few-row kernel multiplies the scores of a run of 4 keys by their
+//   scale, exactly. V, and K in the many-row kernel: converted to multiples of
+//   2^E, E the largest exponent that the wave's keys have had so far (what was
+//   summed in units of an older E is scaled down when it grows).
+// FP16 holds a code below 2^E exactly down to 2^-15 of it, BF16 any that count.
+// Where exponents differ by more than kSpread the tile is summed again key by
+// key in FP32, so that a row is as exact as its own keys allow whatever other
+// rows of its tile see. Exponents up to kTiny do not count for that: FP16
+// results below 2^-25 are 0 (values up to 448 2^-35; of K up to kTinyKey, since
+// any q leaves a score of such keys under 2^-26); in BF16 they are those that an
+// append gives to zeros.
+template <class T> struct Eight;
+template <> struct Eight<_Float16> {
+  static constexpr int kSpread = 15, kTiny = 127 - 35, kTinyKey = 127 - 60;
+  static __device__ __forceinline__ uint32_t pair(uint32_t codes, float scale, bool high) {
+    return high ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes, scale, true))
+                : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes, scale, false));
+  }
+};
+template <> struct Eight<__bf16> {
+  static constexpr int kSpread = 60, kTiny = 127 - 96, kTinyKey = 127 - 96;
+  static __device__ __forceinline__ uint32_t pair(uint32_t codes, float scale, bool high) {
+    return high ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, scale, true))
+                : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, scale, false));
+  }
+};
+// 8 codes as 8 halves
+template <class T>
+__device__ __forceinline__ dword4 eight(uint32_t lo, uint32_t hi, float scale) {
+  return dword4{Eight<T>::pair(lo, scale, false), Eight<T>::pair(lo, scale, true), Eight<T>::pair(hi, scale, false),
+                Eight<T>::pair(hi, scale, true)};
+}
+// 2^(e - to) for e <= to, which is never 0: under 2^-126 it makes no difference
+__device__ __forceinline__ float below(int e, int to) {
+  const int d = e - to + 127;
+  return __builtin_bit_cast(float, (uint32_t)(d < 1 ? 1 : d) << 23);
+}
+// The factor of scores whose keys have the exponent e (biased): a normal number,
+// so that -inf stays what it is.
+__device__ __forceinline__ float score_scale(float scale2, int e) {
+  const float x = __builtin_amdgcn_ldexpf(scale2, e - 127);
+  return fminf(fmaxf(x, 0x1p-126f), 0x1.fffffep127f);
+}
 
 // What lanes read in the place of a key that is not there, as wide as a row:
 // V's rows have to be zeros even where their weight is 0 (0 * NaN), K's may be
@@ -131,10 +182,15 @@ __device__ __forceinline__ float max_x32(float x) { const Two t = both_x32(x); r
 __device__ __forceinline__ float max_x16(float x) { const Two t = both_x16(x); return fmaxf(t.a, t.b); }
 __device__ __forceinline__ float sum_x32(float x) { const Two t = both_x32(x); return t.a + t.b; }
 __device__ __forceinline__ float sum_x16(float x) { const Two t = both_x16(x); return t.a + t.b; }
+// the largest of a small whole number over the wave's groups of 16 lanes
+__device__ __forceinline__ int top_of_groups(int x) {
+  const float f = __builtin_bit_cast(float, x + 0x3f800000);   // as a float of the same order
+  return __builtin_bit_cast(int, max_x32(max_x16(f))) - 0x3f800000;
+}
 
 // The tile of a workgroup. Up to 64 sequences: every lane reads one's lengths,
 // so that one round trip to memory gives all there is to know.
-template <int M>
+template <int M, bool WINDOW = false>
 __device__ __forceinline__ bool find_tile(const TileView& p, int block, int slot, int split, Tile& t) {
   const int count = p.seq.count;
   if (count <= 64) {
@@ -142,11 +198,11 @@ __device__ __forceinline__ bool find_tile(const TileView& p, int block, int slot
     const int first = p.seq.start(i), next = p.seq.start(i + 1), ctx = p.seq.ctx(i);
     const int holds = __popcll(__ballot(lane < count && slot_base(p, i, first, M) <= slot));
     const int s = holds < 1 ? 0 : holds - 1;
-    return make_tile(p, M, block, s, __builtin_amdgcn_readlane(first, s), __builtin_amdgcn_readlane(next, s),
+    return make_tile<WINDOW>(p, M, block, s, __builtin_amdgcn_readlane(first, s), __builtin_amdgcn_readlane(next, s),
                      __builtin_amdgcn_readlane(ctx, s), slot, split, t);
   }
   const int s = wave_upper(count, slot, [&](int i) { return slot_base(p, i, p.seq.start(i), M); });
-  return make_tile(p, M, block, s, p.seq.start(s), p.seq.start(s + 1), p.seq.ctx(s), slot, split, t);
+  return make_tile<WINDOW>(p, M, block, s, p.seq.start(s), p.seq.start(s + 1), p.seq.ctx(s), slot, split, t);
 }
 
 __device__ __forceinline__ bool not_finite(float x) { return !(__builtin_fabsf(x) < __builtin_inff()); }

@@ -8,6 +8,7 @@ constexpr int kMaxSplits = 256, kJoinLanes = 256;
 
 // How many parts the context of a row (token, query head) has; 0 for a row of
 // no sequence. Lanes of a wave may have rows of different tokens.
+template <bool WINDOW>
 __device__ __forceinline__ int parts_of(const AttendParams& p, int64_t at, int tile_rows, int block) {
   const int all = p.heads * p.group, tok = (int)(at / all), hq = (int)(at % all);
   int lo = 0, n = p.seq.count;
@@ -25,10 +26,10 @@ __device__ __forceinline__ int parts_of(const AttendParams& p, int64_t at, int t
   if (tok < t.first || tok >= next) return 0;
   t.rows = t.n * p.group;
   t.row0 = ((tok - t.first) * p.group + hq % p.group) / tile_rows * tile_rows;
-  tile_keys(p, tile_rows, block, ctx, 0, t);
+  tile_keys<WINDOW>(p, tile_rows, block, ctx, 0, t);
   // key1 of split 0 is the length of a part (or all there is); a tile without
   // a key has no part, and its rows are zeros
-  return t.key1 > 0 ? (t.end + t.key1 - 1) / t.key1 : -1;
+  return t.key1 > 0 ? (t.keys + t.key1 - 1) / t.key1 : -1;
 }
 template <class T>
 __device__ __forceinline__ void store_row(const AttendParams& p, int64_t at, int d, f32x4 x) {
@@ -42,7 +43,7 @@ __device__ __forceinline__ void store_row(const AttendParams& p, int64_t at, int
 // Bound by round trips: a row's first parts and all statistics are read before
 // it is known how many there are (the workspace has room for `splits` of every
 // row; what no part wrote is read and not used).
-template <class T, int DP>
+template <class T, int DP, bool WINDOW>
 __global__ void __launch_bounds__(kJoinLanes) attend_join_kernel(AttendParams p, int tile_rows, int block) {
   constexpr int PER = DP / 4, GROUPS = kJoinLanes / PER, AHEAD = 4, STATS = (kMaxSplits + 63) / 64;
   __shared__ float weight[kMaxSplits];
@@ -66,7 +67,7 @@ __global__ void __launch_bounds__(kJoinLanes) attend_join_kernel(AttendParams p,
     m[k] = st[0];
     l[k] = st[1];
   }
-  const int parts = parts_of(p, at, tile_rows, block);
+  const int parts = parts_of<WINDOW>(p, at, tile_rows, block);
   if (parts == 0) return;
 
   if (tid < 64) {
@@ -113,7 +114,7 @@ __global__ void __launch_bounds__(kJoinLanes) attend_join_kernel(AttendParams p,
 
 // Many rows with few parts each: DP/4 lanes a row, which read its statistics
 // and its parts all at once, eight parts at a time.
-template <class T, int DP>
+template <class T, int DP, bool WINDOW>
 __global__ void __launch_bounds__(kJoinLanes) attend_join_rows_kernel(AttendParams p, int tile_rows, int block) {
   constexpr int PER = DP / 4, ROWS = kJoinLanes / PER, AHEAD = 8;
   const int64_t rows = (int64_t)p.seq.tokens * p.heads * p.group, at = (int64_t)blockIdx.x * ROWS + threadIdx.x / PER;
@@ -134,7 +135,7 @@ __global__ void __launch_bounds__(kJoinLanes) attend_join_rows_kernel(AttendPara
       s[k] = st[2 * i + 1];
       v[k] = *(const f32x4*)(from + (int64_t)i * p.dim);
     }
-    if (i0 == 0) parts = parts_of(p, mine, tile_rows, block);
+    if (i0 == 0) parts = parts_of<WINDOW>(p, mine, tile_rows, block);
     float to = top;
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) to = i0 + k < parts ? fmaxf(to, m[k]) : to;

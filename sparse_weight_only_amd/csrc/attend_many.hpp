@@ -1,5 +1,7 @@
 // Attention of many rows (a chunk of a prompt) over a paged cache.
 #pragma once
+#include <type_traits>
+
 #include "attend_device.hpp"
 
 namespace sgemv_dev {
@@ -31,8 +33,17 @@ template <int DP> constexpr int kManyLds = kManyStages * 2 * kManyBlock<DP> * DP
 // different keys, fall on different banks. V's operand, 4 keys of one column a
 // lane, is read with the transposing LDS load: of its 16 lanes, lane 4 i + j
 // names key i's columns 4 j .., and lane c gets column c of the 4 keys.
-template <class T, int DP, bool WHOLE, bool HALVES>
+//
+// EIGHT: the cache holds codes of 8 bits. They come through registers, two to
+// three blocks ahead, are converted once for all waves and written to the same
+// places of LDS (every wave converting what it reads would take as many vector
+// operations as its softmax). Each wave brings 8 keys of a block (4 of the
+// widest), which share their exponents; of the block's others it reads the
+// exponents alone, so that all waves agree on the units.
+// WINDOW: key numbers leave out what no row of the tile sees.
+template <class T, int DP, bool WHOLE, bool HALVES, bool EIGHT, bool WINDOW>
 struct Many {
+  using Elem = std::conditional_t<EIGHT, uint8_t, uint16_t>;
   static constexpr int W = kManyWaves, ST = kManyStages, B = kManyBlock<DP>;
   static constexpr int KC = DP / 16, OT = DP / 32;
   static constexpr int NS = B / 32 / (HALVES ? 2 : 1), KS = 2 * NS;   // 32-key and 16-key steps of a wave in a block
@@ -46,7 +57,8 @@ struct Many {
 
   const AttendParams& p;
   const Tile& t;
-  const uint16_t *kh, *vh;
+  const Elem *kh, *vh;
+  const uint16_t* eh;                                    // EIGHT: the head's exponents
   uint32_t lds;                                          // LDS address of the stages
   const uint16_t* lds_p;
   int lane, wave, c, h;                                  // lane = c + 32 h: row c of the wave
@@ -57,6 +69,10 @@ struct Many {
   dword4 w[KS];                                          // weights of a block, as the second product takes them
   f32x16 o[OT];
   float m, l;
+  int from;                                              // WINDOW: the first slot behind the sinks that the row sees
+  // EIGHT (exponents are biased): what `o` is in units of; the largest of K and
+  // of V so far, which is what LDS holds a block in units of; the least that count
+  int unit, k_top, v_top, k_least, v_least;
 
   __device__ __forceinline__ Many(const AttendParams& p_, const Tile& t_, int head, uint16_t* lds_) : p(p_), t(t_), lds_p(lds_) {
     lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint16_t*)lds_;
@@ -64,8 +80,9 @@ struct Many {
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     c = lane & 31;
     h = lane >> 5;
-    kh = p.k + head * p.k_head;
-    vh = p.v + head * p.v_head;
+    kh = (const Elem*)p.k + head * p.k_head;
+    vh = (const Elem*)p.v + head * p.v_head;
+    eh = EIGHT ? p.exps + head : nullptr;
     part = HALVES ? wave / (W / 2) : 0;
     row0 = t.row0 + 32 * (HALVES ? wave % (W / 2) : wave);
     row = row0 + c < t.rows ? row0 + c : t.rows - 1;
@@ -75,7 +92,10 @@ struct Many {
       const int d = 16 * i + 8 * h;
       q[i] = load<dword4>(or_nothing(WHOLE || d < p.dim, addr(qr + d)));
     }
+    from = WINDOW ? window_from(p, t, row / p.group) : 0;
   }
+
+  __device__ __forceinline__ int slot(int key) const { return slot_of<WINDOW>(t, key); }
 
   // Pages of the rows that this wave fetches of the block at kb (past the end:
   // the last key's). The rows of one load lie in one page (pages hold at least
@@ -87,7 +107,7 @@ struct Many {
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
       const int key = kb + (i * W + wave) * ROWS;
-      w.at[i] = table[__builtin_amdgcn_readfirstlane((key < t.key1 ? key : t.key1 - 1) >> p.seq.page_shift)];
+      w.at[i] = table[__builtin_amdgcn_readfirstlane(slot(key < t.key1 ? key : t.key1 - 1) >> p.seq.page_shift)];
     }
     return w;
   }
@@ -101,9 +121,9 @@ struct Many {
     for (int i = 0; i < LOADS; ++i) {
       const int first = (i * W + wave) * ROWS, key = first + row;
       const int dk = (piece ^ k_mix(key)) * 8, dv = (piece ^ v_mix(key)) * 8;
-      const int pg = w.at[i], slot = (kb + first) & in_page;
+      const int pg = w.at[i], at = (slot(kb) + first) & in_page;
       const bool ok = p.seq.page_ok(pg);
-      const addr_t kr = addr(kh + element(pg, p.k_page, slot, p.k_slot)), vr = addr(vh + element(pg, p.v_page, slot, p.v_slot));
+      const addr_t kr = addr(kh + element(pg, p.k_page, at, p.k_slot)), vr = addr(vh + element(pg, p.v_page, at, p.v_slot));
       const uint32_t ko = 2 * (row * p.k_slot + dk), vo = 2 * (row * p.v_slot + dv);
       if (full && ok) {
         to_lds(kr, ko, ks + first * DP * 2);
@@ -130,24 +150,33 @@ struct Many {
     uint64_t bits = n >= 64 ? ~0ull : (1ull << n) - 1;
     if (!sound) {
       const int key = kb + lane;
-      bits &= __ballot(p.seq.page_ok(t.pages[(key < t.key1 ? key : t.key1 - 1) >> p.seq.page_shift]));
+      bits &= __ballot(p.seq.page_ok(t.pages[slot(key < t.key1 ? key : t.key1 - 1) >> p.seq.page_shift]));
     }
     return B == 64 ? bits : bits | ~0ull << 32;
   }
   __device__ __forceinline__ bool pages_sound() const {
-    const int last = (t.key1 - 1) >> p.seq.page_shift;
+    const int last = slot(t.key1 - 1) >> p.seq.page_shift;
     bool ok = true;
 #pragma unroll 4
-    for (int i = (t.key0 >> p.seq.page_shift) + lane; i <= last; i += 64) ok &= p.seq.page_ok(t.pages[i]);
+    for (int i = (slot(t.key0) >> p.seq.page_shift) + lane; i <= last; i += 64) {
+      // pages that a window leaves out altogether may have been given back
+      if (WINDOW && (int64_t)i << p.seq.page_shift >= t.gap0 && (int64_t)(i + 1) << p.seq.page_shift <= (int64_t)t.gap0 + t.gap) continue;
+      ok &= p.seq.page_ok(t.pages[i]);
+    }
     return __all(ok);
   }
 
+  // bit b: whether the lane's row sees key number kb + b
+  __device__ __forceinline__ uint32_t visible(int kb) const {
+    const uint32_t bits = visible_bits(p, t, row / p.group, slot(kb));
+    return WINDOW ? bits & window_bits(p.sinks, from, slot(kb)) : bits;
+  }
   // -inf for the keys of the block at kb that the lane's row does not see
   __device__ __forceinline__ void mask(int kb, uint64_t there) {
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
       const int at = 32 * (i + part);
-      const uint32_t bits = (visible_bits(p, t, row / p.group, kb + at) & (uint32_t)(there >> at)) >> (4 * h);
+      const uint32_t bits = (visible(kb + at) & (uint32_t)(there >> at)) >> (4 * h);
 #pragma unroll
       for (int e = 0; e < 16; ++e)
         if (!(bits >> (8 * (e / 4) + e % 4) & 1u)) s[i][e] = -__builtin_inff();
@@ -181,12 +210,12 @@ struct Many {
 
   // w = the weights of the block at kb from its scores, and m and the sum with
   // it
-  __device__ __forceinline__ void softmax(int kb, uint64_t there) {
-    if (kb + B > t.full || there != ~0ull) mask(kb, there);
+  __device__ __forceinline__ void softmax(int kb, uint64_t there, float scale2) {
+    if (needs_mask<WINDOW>(p, t, slot(kb), B) || there != ~0ull) mask(kb, there);
     float top = s[0][0];
 #pragma unroll
     for (int e = 1; e < 16 * NS; ++e) top = fmaxf(top, s[e / 16][e % 16]);
-    top = __builtin_fmaf(max_x32(top), p.scale2, -Half<T>::kLift);
+    top = __builtin_fmaf(max_x32(top), scale2, -Half<T>::kLift);
     if (__any(top > m + kSlack)) {
       const float to = fmaxf(m, top), by = m == to ? 1.0f : exp2_fast(m - to);
       l *= by;
@@ -198,8 +227,8 @@ struct Many {
     float sum[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int e = 0; e < 16 * NS; e += 2) {
-      const float a = exp2_fast(__builtin_fmaf(s[e / 16][e % 16], p.scale2, -base));
-      const float b = exp2_fast(__builtin_fmaf(s[e / 16][e % 16 + 1], p.scale2, -base));
+      const float a = exp2_fast(__builtin_fmaf(s[e / 16][e % 16], scale2, -base));
+      const float b = exp2_fast(__builtin_fmaf(s[e / 16][e % 16 + 1], scale2, -base));
       const uint32_t ab = Half<T>::pack(a, b);
       sum[e / 2 % 2] = Half<T>::sum(ab, sum[e / 2 % 2]);
       w[e / 8][e % 8 / 2] = ab;
@@ -257,18 +286,18 @@ struct Many {
     for (int i = 0; i < OT; ++i) o[i] = f32x16{};
     const float base = m == -__builtin_inff() ? 0.0f : m;
     for (int kb = t.key0 + 32 * part; kb < t.key1; kb += HALVES ? 64 : 32) {
-      const int mine = kb + c;
-      const int page = mine < t.key1 ? t.pages[mine >> p.seq.page_shift] : -1;
+      const int mine = kb + c, at = slot(mine);
+      const int page = mine < t.key1 ? t.pages[at >> p.seq.page_shift] : -1;
       const bool ok = p.seq.page_ok(page);
       const uint32_t there = (uint32_t)__ballot(ok);
-      const uint16_t* kr = kh + element(page, p.k_page, mine & in_page, p.k_slot);
+      const Elem* kr = kh + element(page, p.k_page, at & in_page, p.k_slot);
       f32x16 x = f32x16{};
 #pragma unroll
       for (int j = 0; j < KC; ++j) {
         const int d = 16 * j + 8 * h;
         x = Half<T>::mma32(load<dword4>(or_nothing(ok && (WHOLE || d < p.dim), addr(kr + d))), q[j], x);
       }
-      const uint32_t bits = visible_bits(p, t, row / p.group, kb) & there;
+      const uint32_t bits = visible(kb) & there;
       for (int key = 0; key < 32; ++key) {
         // this key's score for row c, from the half that holds it
         const int e = key / 8 * 4 + key % 4;
@@ -278,7 +307,7 @@ struct Many {
         sk = __shfl(sk, c + 32 * (key / 4 % 2));
         const int pg = __shfl(page, key);
         if (!(there >> key & 1u)) continue;
-        const uint16_t* vr = vh + element(pg, p.v_page, (kb + key) & in_page, p.v_slot);
+        const Elem* vr = vh + element(pg, p.v_page, slot(kb + key) & in_page, p.v_slot);
         const float pk = exp2_fast(__builtin_fmaf(sk, p.scale2, -base));
         if (bits >> key & 1u) {
 #pragma unroll
@@ -295,6 +324,280 @@ struct Many {
             }
         }
       }
+    }
+  }
+
+  // ---- EIGHT
+  static constexpr int CP = DP == 64 ? 8 : 16;           // codes of a lane's piece
+  static constexpr int ROW_LANES = DP / CP;
+  static constexpr int WAVE_KEYS = 64 / ROW_LANES;       // keys of a block that a wave brings
+  static constexpr int GROUPS = B / 8;                   // 8 keys in a row share their page and their exponents
+  using Piece = std::conditional_t<DP == 64, dword2, dword4>;
+  struct Raw {
+    Piece k, v;
+    uint32_t e;                                          // exponents of group lane % GROUPS
+  };
+  struct Units { int k, v; };                            // what a stage holds K and V in units of
+
+  // the page of group lane % GROUPS of the block at kb (past the end: of the last key)
+  __device__ __forceinline__ int lookup8(int kb) const {
+    const int key = kb + 8 * (lane % GROUPS);
+    return t.pages[slot(key < t.key1 ? key : t.key1 - 1) >> p.seq.page_shift];
+  }
+  __device__ __forceinline__ addr_t exps_at(int page, int at) const {
+    const int in_page = (1 << p.seq.page_shift) - 1;
+    return addr(eh + ((uint64_t)(uint32_t)page * p.exp_page + (uint64_t)(uint32_t)((at & in_page) >> p.exp_shift) * (uint32_t)p.heads));
+  }
+  // starts the loads of the block at kb; `pages` from lookup8(kb)
+  __device__ __forceinline__ void fetch8(int kb, int pages, Raw& x) const {
+    const int in_page = (1 << p.seq.page_shift) - 1;
+    const int first = wave * WAVE_KEYS, key = lane / ROW_LANES, d = lane % ROW_LANES * CP;
+    const int pg = __builtin_amdgcn_readlane(pages, first / 8), at = (slot(kb) + first) & in_page;
+    const bool in = p.seq.page_ok(pg) && kb + first + key < t.key1 && (WHOLE || d < p.dim);
+    x.k = load<Piece>(or_nothing(in, addr(kh + element(pg, p.k_page, at, p.k_slot)) + (key * p.k_slot + d)));
+    x.v = load<Piece>(or_nothing(in, addr(vh + element(pg, p.v_page, at, p.v_slot)) + (key * p.v_slot + d)));
+    // a group that is not there, or that no row sees, has no exponents
+    const int gk = kb + 8 * (lane % GROUPS), ga = slot(gk);
+    const bool ok = gk < t.key1 && p.seq.page_ok(pages) && (!WINDOW || ga < p.sinks || ga + 7 >= t.low);
+    x.e = load<uint16_t>(or_nothing(ok, exps_at(pages, ga)));
+  }
+  // converts a block that has come into a stage
+  __device__ __forceinline__ Units convert(const Raw& x, int stage) {
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) {
+      const int e = __builtin_amdgcn_readlane(x.e, g), ek = e & 255, ev = e >> 8;
+      k_top = ek > k_top ? ek : k_top;
+      v_top = ev > v_top ? ev : v_top;
+      k_least = ek > Eight<T>::kTinyKey && ek < k_least ? ek : k_least;
+      v_least = ev > Eight<T>::kTiny && ev < v_least ? ev : v_least;
+    }
+    const int mine = __builtin_amdgcn_readlane(x.e, wave * WAVE_KEYS / 8);
+    const float by_k = below(mine & 255, k_top), by_v = below(mine >> 8, v_top);
+    const int key = wave * WAVE_KEYS + lane / ROW_LANES, piece = lane % ROW_LANES * (CP / 8);
+    const uint32_t ks = lds + stage * 4 * STAGE + key * DP * 2, vs = ks + STAGE * 2;
+#pragma unroll
+    for (int u = 0; u < CP / 8; ++u) {
+      lds_store(ks + ((piece + u) ^ k_mix(key)) * 16, eight<T>(x.k[2 * u], x.k[2 * u + 1], by_k));
+      lds_store(vs + ((piece + u) ^ v_mix(key)) * 16, eight<T>(x.v[2 * u], x.v[2 * u + 1], by_v));
+    }
+    return Units{k_top, v_top};
+  }
+  static __device__ __forceinline__ void lds_store(uint32_t at, dword4 x) { *(__attribute__((address_space(3))) dword4*)at = x; }
+  // takes the sums to the units of a block
+  __device__ __forceinline__ void take(int to) {
+    if (to == unit) return;
+    const float by = below(unit, to);
+#pragma unroll
+    for (int i = 0; i < OT; ++i) o[i] *= by;
+    unit = to;
+  }
+
+  // All of it again, in FP32 from the keys' own scales: scores, the maximum and
+  // the sums, each row adding the keys it sees and no other. Only for a wave
+  // whose sums are not finite or whose exponents lie too far apart.
+  __device__ __forceinline__ void walk_seen_only8() {
+    const int in_page = (1 << p.seq.page_shift) - 1;
+#pragma unroll
+    for (int i = 0; i < OT; ++i) o[i] = f32x16{};
+    m = -__builtin_inff();
+    l = 0.0f;
+    unit = 127;
+    for (int kb = t.key0 + 32 * part; kb < t.key1; kb += HALVES ? 64 : 32) {
+      const int mine = kb + c, at = slot(mine);
+      const int page = mine < t.key1 ? t.pages[at >> p.seq.page_shift] : -1;
+      const bool ok = p.seq.page_ok(page);
+      const uint32_t there = (uint32_t)__ballot(ok);
+      const uint32_t e = load<uint16_t>(or_nothing(ok, exps_at(page, at)));
+      const Elem* kr = kh + element(page, p.k_page, at & in_page, p.k_slot);
+      f32x16 x = f32x16{};
+#pragma unroll
+      for (int j = 0; j < KC; ++j) {
+        const int d = 16 * j + 8 * h;
+        const dword2 w8 = load<dword2>(or_nothing(ok && (WHOLE || d < p.dim), addr(kr + d)));
+        x = Half<T>::mma32(eight<T>(w8.x, w8.y, 1.0f), q[j], x);
+      }
+      const uint32_t bits = visible(kb) & there, own = bits >> (4 * h);
+      float top = -__builtin_inff();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float by = score_scale(p.scale2, __builtin_amdgcn_readlane(e, i / 4 * 8) & 255);
+        x[i] = own >> (8 * (i / 4) + i % 4) & 1u ? x[i] * by : -__builtin_inff();
+        top = fmaxf(top, x[i]);
+      }
+      top = max_x32(top);
+      const float to = fmaxf(m, top), by = m == to ? 1.0f : exp2_fast(m - to);
+      l *= by;
+#pragma unroll
+      for (int i = 0; i < OT; ++i) o[i] *= by;
+      m = to;
+      const float base = m == -__builtin_inff() ? 0.0f : m;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        x[i] = exp2_fast(x[i] - base);
+        if (own >> (8 * (i / 4) + i % 4) & 1u) l += x[i];
+      }
+      for (int key = 0; key < 32; ++key) {
+        const int n = key / 8 * 4 + key % 4;
+        float pk = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) pk = i == n ? x[i] : pk;
+        pk = __shfl(pk, c + 32 * (key / 4 % 2));
+        const int pg = __shfl(page, key), ev = (int)(__shfl(e, key) >> 8) - 127;
+        if (!(there >> key & 1u)) continue;
+        const Elem* vr = vh + element(pg, p.v_page, slot(kb + key) & in_page, p.v_slot);
+        if (bits >> key & 1u) {
+#pragma unroll
+          for (int i = 0; i < OT; ++i)
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+              const int d = 32 * i + 8 * a + 4 * h;
+              if (d >= p.dim) continue;
+              const uint32_t w4 = load<uint32_t>(addr(vr + d));
+              const uint32_t lo = Eight<T>::pair(w4, 1.0f, false), hi = Eight<T>::pair(w4, 1.0f, true);
+              o[i][4 * a] += pk * __builtin_amdgcn_ldexpf(Half<T>::lo(lo), ev);
+              o[i][4 * a + 1] += pk * __builtin_amdgcn_ldexpf(Half<T>::hi(lo), ev);
+              o[i][4 * a + 2] += pk * __builtin_amdgcn_ldexpf(Half<T>::lo(hi), ev);
+              o[i][4 * a + 3] += pk * __builtin_amdgcn_ldexpf(Half<T>::hi(hi), ev);
+            }
+        }
+      }
+    }
+  }
+
+  // As walk() below; a wave's loads need no wait of their own.
+  __device__ __forceinline__ void walk8() {
+    m = -__builtin_inff();
+    l = 0.0f;
+    unit = k_top = v_top = 0;
+    k_least = v_least = 255;
+#pragma unroll
+    for (int i = 0; i < OT; ++i) o[i] = f32x16{};
+    if (t.key0 >= t.key1) return;
+    const bool live = row0 < t.rows;
+    const int blocks = (t.key1 - t.key0 + B - 1) / B;
+    Raw even, odd;                                       // blocks on their way, by their numbers
+    Units before = {0, 0}, now, next = {0, 0};           // of blocks i - 1, i, i + 1
+    int pages;
+    {
+      const int a = lookup8(t.key0), b = lookup8(t.key0 + B), d = lookup8(t.key0 + 2 * B);
+      fetch8(t.key0, a, even);
+      fetch8(t.key0 + B, b, odd);
+      pages = lookup8(t.key0 + 3 * B);
+      now = convert(even, 0);
+      fetch8(t.key0 + 2 * B, d, even);
+    }
+    const bool sound = pages_sound();
+    // block i + 1 into LDS, block i + 3 on its way, the pages of block i + 4
+    // (asked for first: loads return in order)
+    const auto ahead = [&](int i, Raw& r) {
+      const int later = lookup8(t.key0 + (i + 4) * B);
+      next = convert(r, (i + 1) % ST);
+      fetch8(t.key0 + (i + 3) * B, pages, r);
+      pages = later;
+    };
+    const auto begin = [&] { change_over<63>(); };
+    const auto change = [&] { change_over<63>(); };
+    const auto weigh = [&](int i, const Units& u) {
+      softmax(t.key0 + i * B, there(t.key0 + i * B, sound), score_scale(p.scale2, u.k));
+    };
+    const auto shift = [&] {
+      before = now;
+      now = next;
+    };
+    if (!live) {
+      const auto step = [&](int i, Raw& r) {
+        begin();
+        ahead(i, r);
+        change();
+      };
+      for (int i = 0; i <= blocks; i += 2) {
+        step(i, odd);
+        if (i < blocks) step(i + 1, even);
+      }
+    } else if (wave < W / 2) {
+      begin();
+      first_product(0);
+      change();
+      ahead(0, odd);
+      weigh(0, now);
+      shift();
+      const auto step = [&](int i, Raw& r) {
+        begin();
+        take(before.v);
+        products((i - 1) % ST, i % ST);
+        change();
+        ahead(i, r);
+        weigh(i, now);
+        shift();
+      };
+      for (int i = 1; i < blocks; i += 2) {
+        step(i, even);
+        if (i + 1 < blocks) step(i + 1, odd);
+      }
+      begin();
+      take(before.v);
+      second_product((blocks - 1) % ST);
+      change();
+    } else {
+      begin();
+      ahead(0, odd);
+      change();
+      first_product(0);
+      shift();
+      const auto step = [&](int i, Raw& r) {
+        begin();
+        ahead(i, r);
+        weigh(i - 1, before);
+        change();
+        take(before.v);
+        products((i - 1) % ST, i % ST);
+        shift();
+      };
+      for (int i = 1; i < blocks; i += 2) {
+        step(i, even);
+        if (i + 1 < blocks) step(i + 1, odd);
+      }
+      begin();
+      weigh(blocks - 1, before);
+      change();
+      take(before.v);
+      second_product((blocks - 1) % ST);
+    }
+    if (live) {
+      bool bad = k_top - k_least > Eight<T>::kSpread || v_top - v_least > Eight<T>::kSpread;
+#pragma unroll
+      for (int i = 0; i < OT; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) bad |= not_finite(o[i][e]);
+      if (__any(bad)) walk_seen_only8();
+      l = sum_x32(l);
+      const int by = unit - 127;
+#pragma unroll
+      for (int i = 0; i < OT; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[i][e] = __builtin_amdgcn_ldexpf(o[i][e], by);
+    }
+    if (HALVES) join_halves(live);
+  }
+
+  // HALVES: the second half's sums go to the first's waves, a lane's values 64 floats apart
+  __device__ __forceinline__ void join_halves(bool live) {
+    float* x = (float*)lds_p + (wave % (W / 2)) * (16 * OT + 2) * 64 + lane;
+    __syncthreads();
+    if (part == 1 && live) {
+      x[0] = m;
+      x[64] = l;
+#pragma unroll
+      for (int i = 0; i < 16 * OT; ++i) x[(i + 2) * 64] = o[i / 16][i % 16];
+    }
+    __syncthreads();
+    if (part == 0 && live) {
+      const float m1 = x[0], to = fmaxf(m, m1);
+      const float by0 = m == to ? 1.0f : exp2_fast(m - to), by1 = m1 == to ? 1.0f : exp2_fast(m1 - to);
+      l = by0 * l + by1 * x[64];
+#pragma unroll
+      for (int i = 0; i < 16 * OT; ++i) o[i / 16][i % 16] = by0 * o[i / 16][i % 16] + by1 * x[(i + 2) * 64];
+      m = to;
     }
   }
 
@@ -336,7 +639,7 @@ struct Many {
     // block i is there: only the loads of block i + 1 may still be on their way
     const auto begin = [&] { change_over<2 * LOADS>(); };
     const auto change = [&] { change_over<63>(); };
-    const auto weigh = [&](int i) { softmax(t.key0 + i * B, there(t.key0 + i * B, sound)); };
+    const auto weigh = [&](int i) { softmax(t.key0 + i * B, there(t.key0 + i * B, sound), p.scale2); };
     if (!live) {
       for (int i = 0; i <= blocks; ++i) {
         begin();
@@ -387,26 +690,7 @@ struct Many {
       if (__any(bad)) walk_seen_only();
       l = sum_x32(l);
     }
-    if (HALVES) {
-      // the second half's sums, a lane's values 64 floats apart
-      float* x = (float*)lds_p + (wave % (W / 2)) * (16 * OT + 2) * 64 + lane;
-      __syncthreads();
-      if (part == 1 && live) {
-        x[0] = m;
-        x[64] = l;
-#pragma unroll
-        for (int i = 0; i < 16 * OT; ++i) x[(i + 2) * 64] = o[i / 16][i % 16];
-      }
-      __syncthreads();
-      if (part == 0 && live) {
-        const float m1 = x[0], to = fmaxf(m, m1);
-        const float by0 = m == to ? 1.0f : exp2_fast(m - to), by1 = m1 == to ? 1.0f : exp2_fast(m1 - to);
-        l = by0 * l + by1 * x[64];
-#pragma unroll
-        for (int i = 0; i < 16 * OT; ++i) o[i / 16][i % 16] = by0 * o[i / 16][i % 16] + by1 * x[(i + 2) * 64];
-        m = to;
-      }
-    }
+    if (HALVES) join_halves(live);
   }
 
   __device__ __forceinline__ void store(int head, int split) const {
@@ -444,17 +728,18 @@ struct Many {
   }
 };
 
-template <class T, int DP, bool WHOLE, bool HALVES>
+template <class T, int DP, bool WHOLE, bool HALVES, bool EIGHT, bool WINDOW>
 __global__ void __launch_bounds__(64 * kManyWaves, DP == 64 ? 4 : 2) attend_many_kernel(AttendParams p) {
   extern __shared__ __attribute__((aligned(16))) uint16_t many_lds[];
   const int id = blockIdx.x, head = id % p.heads, split = id / p.heads % p.splits;
   // the last rows of a prompt see the most keys: they go first
   const int slot = p.slots - 1 - id / p.heads / p.splits;
   Tile t;
-  if (!find_tile<kManyRows<HALVES>>(p, kManyBlock<DP>, slot, split, t)) return;
+  if (!find_tile<kManyRows<HALVES>, WINDOW>(p, kManyBlock<DP>, slot, split, t)) return;
   if (p.splits > 1 && t.key0 >= t.key1) return;
-  Many<T, DP, WHOLE, HALVES> f(p, t, head, many_lds);
-  f.walk();
+  Many<T, DP, WHOLE, HALVES, EIGHT, WINDOW> f(p, t, head, many_lds);
+  if constexpr (EIGHT) f.walk8();
+  else f.walk();
   f.store(head, split);
 }
 

@@ -8,6 +8,7 @@
 namespace sgemv_dev {
 
 typedef uint32_t dword4 __attribute__((ext_vector_type(4)));
+typedef uint32_t dword2 __attribute__((ext_vector_type(2)));
 
 // The last sequence s of [0, count) with f(s) <= x, for f non-decreasing and
 // f(0) <= x (0 otherwise): each step the wave's 64 lanes look at 64 places,

@@ -64,16 +64,29 @@ struct TileView {
   int32_t tree_words;
   int32_t group;          // query heads per cache head
   int32_t splits;         // parts of the context
+  int32_t window, sinks;  // of a windowed attention, each 0 .. 2^30; not looked at by others
 };
 
 struct Tile {
   int s, first, n;          // sequence, its first new token, its new tokens
   int old;                  // slot of its first new token
   int row0, rows;           // first row of the tile, rows of the sequence
-  int end, full;            // keys any row sees, keys every row sees
-  int key0, key1;           // this split's part of [0, end)
+  int end, full;            // slots up to which any row sees keys, up to which every row does
+  int keys;                 // keys to go through: end, less what a window leaves out
+  int key0, key1;           // this split's part of [0, keys)
   const int32_t* pages;
+  // Windowed: rows see the first `sinks` slots and those from a slot of their
+  // own on, which is `low` or more for any row and `all` or less for every
+  // row. Whole blocks in between are left out: key number v is slot v below
+  // gap0 and v + gap from there on (both multiples of the block).
+  int low, all, gap0, gap;
 };
+
+// The slot of key number v of a tile.
+template <bool WINDOW>
+SGEMV_BOTH int slot_of(const Tile& t, int v) {
+  return WINDOW && v >= t.gap0 ? v + t.gap : v;
+}
 
 // First slot of sequence s, whose first new token is `first`. tokens x heads
 // is at most 2^30, so rows fit 32 bits without a sign.
@@ -83,8 +96,10 @@ SGEMV_BOTH int slot_base(const TileView& p, int s, int first, int m) {
 
 // The keys of the tile at `row0` of sequence t.s, and split `split` of them in
 // whole blocks of `block` keys.
+template <bool WINDOW = false>
 SGEMV_BOTH void tile_keys(const TileView& p, int m, int block, int ctx, int split, Tile& t) {
   t.old = ctx - t.n;
+  t.low = t.all = t.gap0 = t.gap = 0;
   if (p.tree) {
     t.end = ctx;
     t.full = t.old;
@@ -94,15 +109,30 @@ SGEMV_BOTH void tile_keys(const TileView& p, int m, int block, int ctx, int spli
     t.full = t.old + t.row0 / p.group + 1;
   }
   t.end = t.end < 0 ? 0 : t.end > ctx ? ctx : t.end;
-  const int blocks = (t.end + block - 1) / block;
+  t.keys = t.end;
+  if (WINDOW) {
+    // of a tree a row sees as many slots before the new tokens as its path
+    // leaves of the window: none to all of them
+    const int last = t.row0 + m < t.rows ? (t.row0 + m - 1) / p.group : t.n - 1;
+    const int low = p.tree ? t.old - p.window : t.old + t.row0 / p.group + 1 - p.window;
+    const int all = p.tree ? (t.n < p.window ? t.old + t.n - p.window : t.old) : t.old + last + 1 - p.window;
+    t.low = low < 0 ? 0 : low > t.end ? t.end : low;
+    t.all = all < 0 ? 0 : all > t.end ? t.end : all;
+    t.gap0 = ((p.sinks < t.end ? p.sinks : t.end) + block - 1) / block * block;
+    const int gap = t.low / block * block - t.gap0;
+    t.gap = gap > 0 ? gap : 0;
+    t.keys = t.end - t.gap;
+  }
+  const int blocks = (t.keys + block - 1) / block;
   const int per = (blocks + p.splits - 1) / p.splits * block;
   const int64_t k0 = (int64_t)split * per;
-  t.key0 = k0 < t.end ? (int)k0 : t.end;
-  t.key1 = k0 + per < t.end ? (int)(k0 + per) : t.end;
+  t.key0 = k0 < t.keys ? (int)k0 : t.keys;
+  t.key1 = k0 + per < t.keys ? (int)(k0 + per) : t.keys;
 }
 
 // The tile of `slot`, which lies in sequence s with new tokens first .. next - 1
 // and ctx tokens in all; false for an empty slot.
+template <bool WINDOW = false>
 SGEMV_BOTH bool make_tile(const TileView& p, int m, int block, int s, int first, int next, int ctx, int slot, int split, Tile& t) {
   t.s = s;
   t.first = first;
@@ -112,7 +142,7 @@ SGEMV_BOTH bool make_tile(const TileView& p, int m, int block, int s, int first,
   if (t.n <= 0 || at < 0 || at * m >= t.rows) return false;
   t.row0 = (int)at * m;
   t.pages = p.seq.pages + s * p.seq.pages_stride;
-  tile_keys(p, m, block, ctx, split, t);
+  tile_keys<WINDOW>(p, m, block, ctx, split, t);
   return true;
 }
 
@@ -135,6 +165,40 @@ SGEMV_BOTH uint32_t seen_bits(const TileView& p, const Tile& t, int i, int kb) {
     n = n < t.end - kb ? n : t.end - kb;
   }
   return n >= 32 ? bits : n <= 0 ? 0u : bits & ((1u << n) - 1u);
+}
+
+// How many new tokens of the tile's sequence new token `i` sees in the tree.
+SGEMV_BOTH int path_of(const TileView& p, const Tile& t, int i) {
+  const uint32_t* w = p.tree + (int64_t)(t.first + i) * p.tree_words;
+  int n = 0;
+  for (int k = 0; k < p.tree_words && 32 * k < t.n; ++k) {
+    const uint32_t bits = t.n - 32 * k >= 32 ? w[k] : w[k] & ((1u << (t.n - 32 * k)) - 1u);
+    n += __builtin_popcount(bits);
+  }
+  return n;
+}
+
+// Windowed: the first slot behind the sinks that new token `i` sees. Of a tree
+// the tokens of its path come off the window first, and are seen even where
+// they are more.
+SGEMV_BOTH int window_from(const TileView& p, const Tile& t, int i) {
+  if (!p.tree) return t.old + i + 1 - p.window;
+  const int path = path_of(p, t, i);
+  return path < p.window ? t.old + path - p.window : t.old;
+}
+
+// Bit b: slot kb + b is one of the first `sinks` or `from` or later.
+SGEMV_BOTH uint32_t window_bits(int sinks, int from, int kb) {
+  const int64_t a = (int64_t)from - kb;
+  const int n = sinks - kb;
+  const uint32_t late = a <= 0 ? ~0u : a >= 32 ? 0u : ~0u << a;
+  return late | (n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u);
+}
+
+// Whether a block of `block` slots at kb holds a slot that some row does not see.
+template <bool WINDOW>
+SGEMV_BOTH bool needs_mask(const TileView& p, const Tile& t, int kb, int block) {
+  return kb + block > t.full || (WINDOW && kb < t.all && kb + block > p.sinks);
 }
 
 // The same for a token that may have no slot: in a sequence shorter than its

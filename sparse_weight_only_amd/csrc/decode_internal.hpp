@@ -40,6 +40,24 @@ inline int check_cache(const sgemv_cache* c, bool written) {
   return SGEMV_OK;
 }
 
+// A cache in 8 bits: 16 codes to a 16-byte access.
+inline bool stride16_ok(int64_t stride, int64_t n, int64_t least) { return n <= 1 || (stride_ok(stride, n, least) && stride % 16 == 0); }
+
+inline int check_cache8(const sgemv_cache8* c, bool written) {
+  if (!c) return SGEMV_EINVAL;
+  if (c->pages < 0 || c->heads < 1 || c->heads > 65535 || !valid_dim(c->head_dim) || c->head_dim % 16) return SGEMV_EINVAL;
+  if (c->page_size < 8 || c->page_size > 65536 || (c->page_size & (c->page_size - 1))) return SGEMV_EINVAL;
+  if (c->scale_slots < 8 || c->scale_slots > 128 || (c->scale_slots & (c->scale_slots - 1)) || c->scale_slots > c->page_size) return SGEMV_EINVAL;
+  const int64_t least = written ? c->head_dim : 0;
+  for (const int64_t* s : {&c->k_page, &c->v_page}) {
+    if (!stride16_ok(s[0], c->pages, least) || !stride16_ok(s[1], c->page_size, least) || !stride16_ok(s[2], c->heads, least)) return SGEMV_EINVAL;
+  }
+  if (c->pages > 0 && (!c->k || !c->v || !c->scales)) return SGEMV_EINVAL;
+  if ((int64_t)(c->page_size / c->scale_slots) * c->heads > INT32_MAX) return SGEMV_ESIZE;
+  if ((uintptr_t)c->k % 16 || (uintptr_t)c->v % 16 || (uintptr_t)c->scales % 2) return SGEMV_EALIGN;
+  return SGEMV_OK;
+}
+
 inline int check_seqs(const sgemv_seqs* s) {
   if (!s || s->count < 0 || s->pages_per_seq < 0) return SGEMV_EINVAL;
   if (s->count == 0) return SGEMV_OK;
@@ -49,7 +67,8 @@ inline int check_seqs(const sgemv_seqs* s) {
   return SGEMV_OK;
 }
 
-inline sgemv_dev::SeqView seq_view(const sgemv_seqs* s, const sgemv_cache* c, int32_t tokens) {
+template <class Cache>
+sgemv_dev::SeqView seq_view(const sgemv_seqs* s, const Cache* c, int32_t tokens) {
   sgemv_dev::SeqView v;
   v.new_start = s->new_start;
   v.ctx_len = s->ctx_len;

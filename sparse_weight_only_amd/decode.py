@@ -1,9 +1,10 @@
 """The operators between the GEMVs of a decode step, on torch tensors.
 
 ``PagedCache.append`` (rotary positions and the append to a paged cache),
-``PagedCache.attend`` (attention of the new tokens over it), ``Rope.apply``
-(rotary positions alone) and ``adjust_logits`` (penalties, biases and grammar
-masks) check their tensors, marshal them into the C ABI's structures
+``PagedCache.attend`` (attention of the new tokens over it, all of it or through
+a window), the same of ``PagedCache8``, which holds 8 bits, ``Rope.apply``
+(rotary positions alone), ``adjust_logits`` (penalties, biases and grammar
+masks) and ``sample`` (the choice of tokens) check their tensors, marshal them into the C ABI's structures
 (``include/sgemv.h``) and enqueue on the current stream or on ``stream``.
 Everything is computed by the library; lengths, page tables and positions are
 read on the device when the kernels run, so a captured call can be replayed
@@ -36,6 +37,13 @@ class Cache(ctypes.Structure):
                 ("pages", _I32), ("page_size", _I32), ("heads", _I32), ("head_dim", _I32), ("dtype", _I32)]
 
 
+class Cache8(ctypes.Structure):
+    """A paged cache in 8 bits (mirrors sgemv_cache8)."""
+    _fields_ = [("k", _P), ("v", _P), ("scales", _P), ("k_page", _I64), ("k_slot", _I64), ("k_head", _I64),
+                ("v_page", _I64), ("v_slot", _I64), ("v_head", _I64),
+                ("pages", _I32), ("page_size", _I32), ("heads", _I32), ("head_dim", _I32), ("scale_slots", _I32)]
+
+
 class Seqs(ctypes.Structure):
     """Sequences and their new tokens (mirrors sgemv_seqs)."""
     _fields_ = [("new_start", _P), ("ctx_len", _P), ("pages", _P), ("pages_stride", _I64),
@@ -64,6 +72,12 @@ class Logits(ctypes.Structure):
                 ("bias_start", _P), ("bias_ids", _P), ("bias_values", _P), ("n_bias", _I64),
                 ("masks", _P), ("mask_stride", _I64), ("mask_row", _P),
                 ("n_masks", _I32), ("rows", _I32), ("vocab", _I32), ("dtype", _I32), ("out_dtype", _I32)]
+
+
+class Sampling(ctypes.Structure):
+    """The choice of a token for rows of logits (mirrors sgemv_sampling)."""
+    _fields_ = [("x", _P), ("x_stride", _I64), ("uniform", _P), ("temperature", _P), ("top_k", _P), ("top_p", _P), ("min_p", _P),
+                ("ids", _P), ("logprob", _P), ("rows", _I32), ("vocab", _I32), ("dtype", _I32)]
 
 
 def rope_table(rot_dim: int, base: float = 10000.0, factor: float = 1.0, context: float = 0.0, low: float = 1.0,
@@ -113,7 +127,7 @@ def _packer(structure):
     return struct.Struct("@" + "".join(codes[t] for _, t in structure._fields_) + "0q").pack
 
 
-_pack_rows, _pack_logits = _packer(Rows), _packer(Logits)
+_pack_rows, _pack_logits, _pack_sampling = _packer(Rows), _packer(Logits), _packer(Sampling)
 
 # torch and what is looked up in it on every call, set by _init (the library's
 # host side is used without torch)
@@ -274,6 +288,16 @@ class PagedCache:
         self.args = Cache(k.data_ptr(), v.data_ptr(), *k.stride()[:3], *v.stride()[:3], *k.shape, _type(k.dtype))
         self._ref, self._index = _byref(self.args), k.get_device()
 
+    def _append(self):
+        return lib().sgemv_append, "sgemv_append"
+
+    def _attend(self, window, sinks):
+        """The entry points of an attention, and what they take behind the arguments that all have."""
+        L = lib()
+        if window or sinks:
+            return L.sgemv_attend_window_plan, L.sgemv_attend_window, (window, sinks), "sgemv_attend_window"
+        return L.sgemv_attend_plan, L.sgemv_attend, (), "sgemv_attend"
+
     def append(self, seqs: Sequences, k, v, rope: Rope = None, q=None, q_out=None, positions=None, stream=None):
         """Store the new tokens' k (turned by ``rope``) and v, [tokens, heads,
         head_dim], in their slots; q [tokens, query heads, head_dim] turned
@@ -301,24 +325,31 @@ class PagedCache:
                 if q_out is None:
                     q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
                 qo = _rows(q_out, "q_out")
-            code = lib().sgemv_append(self._ref, seqs._ref, None if rope is None else rope._ref, at, qr, qo, kr, vr, s)
+            call, name = self._append()
+            code = call(self._ref, seqs._ref, None if rope is None else rope._ref, at, qr, qo, kr, vr, s)
         finally:
             _leave(ctx)
         if code:
-            _check(code, "sgemv_append")
+            _check(code, name)
         return q_out
 
-    def plan(self, seqs: Sequences, tokens: int, heads: int, max_ctx: int = 0) -> AttendPlan:
+    def plan(self, seqs: Sequences, tokens: int, heads: int, max_ctx: int = 0, window: int = 0, sinks: int = 0) -> AttendPlan:
         """The launch that ``attend`` would make (its workspace_bytes, its splits)."""
-        return attend_plan(self.args, seqs.args, tokens, heads, max_ctx)
+        call, _, more, name = self._attend(window, sinks)
+        pl = AttendPlan()
+        _check(call(self._ref, seqs._ref, tokens, heads, *more, max_ctx, _byref(pl)), name + "_plan")
+        return pl
 
     def attend(self, seqs: Sequences, q, scale: float = None, tree=None, out=None, max_ctx: int = 0, workspace=None,
-               stream=None):
+               stream=None, window: int = 0, sinks: int = 0):
         """Attention of the new tokens q [tokens, query heads, head_dim] over
         the cache, which holds them already. scale: 1/sqrt(head_dim) unless
         given. tree (int32 [tokens, words]): bit j of a row says whether it
         sees new token j of its sequence; without it a token sees the slots up
-        to its own. max_ctx: the longest context to expect (shapes the launch
+        to its own. window: of those only the last ``window``, and the first
+        ``sinks`` of the sequence (0: all); with a tree the new tokens that a
+        token sees come off its window first, and none of them is left out.
+        max_ctx: the longest context to expect (shapes the launch
         only). workspace: a uint8 tensor of ``plan(...).workspace_bytes`` or
         more, not shared with calls that may run at the same time; made if
         not given. Rows of no sequence stay as they are in a given ``out``
@@ -342,22 +373,74 @@ class PagedCache:
         try:
             if out is None:
                 out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-            L, c, sq = lib(), self._ref, seqs._ref
+            plan, call, more, name = self._attend(window, sinks)
+            c, sq = self._ref, seqs._ref
             if workspace is None:
                 pl = AttendPlan()
-                code = L.sgemv_attend_plan(c, sq, tokens, heads, max_ctx, _byref(pl))
+                code = plan(c, sq, tokens, heads, *more, max_ctx, _byref(pl))
                 if code:
-                    _check(code, "sgemv_attend_plan")
+                    _check(code, name + "_plan")
                 if pl.workspace_bytes:
                     workspace = torch.empty(pl.workspace_bytes, dtype=torch.uint8, device=dev)
             scratch, room = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
-            code = L.sgemv_attend(c, sq, qr, _rows(out, "out"), dim ** -0.5 if scale is None else scale, at, words, max_ctx,
-                                  scratch, room, s)
+            code = call(c, sq, qr, _rows(out, "out"), dim ** -0.5 if scale is None else scale, at, words, *more, max_ctx,
+                        scratch, room, s)
         finally:
             _leave(ctx)
         if code:
-            _check(code, "sgemv_attend")
+            _check(code, name)
         return out
+
+
+class PagedCache8(PagedCache):
+    """A paged cache in 8 bits: ``k`` and ``v`` are float8_e4m3fn [pages,
+    page_size, heads, head_dim], in units of ``scales``, float8_e8m0fnu [pages,
+    page_size / scale_slots, heads, 2] (K's and V's): ``scale_slots`` slots (a
+    power of two, 8 to 128) share a power of two for each head. Appended rows
+    and queries are FP16 or BF16. A block of ``scale_slots`` slots that gets new
+    tokens is one sequence's alone: sequences that share a prefix share whole
+    blocks of it."""
+
+    def __init__(self, pages: int, page_size: int, heads: int, head_dim: int, scale_slots: int = None, device="cuda"):
+        _init()
+        n = min(32, page_size) if scale_slots is None else scale_slots
+        if n < 1 or page_size % n:
+            raise ValueError(f"pages of {page_size} slots have no whole number of blocks of {n}")
+        bits = torch.zeros((2, pages, page_size, heads, head_dim), dtype=torch.uint8, device=device)
+        scales = torch.full((pages, page_size // n, heads, 2), 31, dtype=torch.uint8, device=device)
+        self._set(*bits.view(torch.float8_e4m3fn), scales.view(torch.float8_e8m0fnu))
+
+    @classmethod
+    def from_tensors(cls, k, v, scales) -> "PagedCache8":
+        """A cache over tensors of the caller's: ``k`` and ``v`` of any strides
+        with contiguous columns, ``scales`` contiguous."""
+        _init()
+        self = cls.__new__(cls)
+        self._set(k, v, scales)
+        return self
+
+    def _set(self, k, v, scales):
+        for what, x in (("k", k), ("v", v)):
+            if x.dim() != 4 or (x.shape[3] > 1 and x.stride(3) != 1) or x.dtype != torch.float8_e4m3fn:
+                raise ValueError(f"{what} must be a float8_e4m3fn tensor [pages, page_size, heads, head_dim] with contiguous columns")
+        if k.shape != v.shape:
+            raise ValueError("k and v differ in shape")
+        pages, page, heads, dim = k.shape
+        n = scales.shape[1] if scales.dim() == 4 else 0
+        if (n < 1 or page % n or scales.shape != (pages, n, heads, 2) or scales.dtype != torch.float8_e8m0fnu
+                or not scales.is_contiguous()):
+            raise ValueError("scales must be a contiguous float8_e8m0fnu tensor [pages, page_size / scale_slots, heads, 2]")
+        _on(k.device, v=v, scales=scales)
+        self.k, self.v, self.scales, self.device = k, v, scales, k.device
+        self.args = Cache8(k.data_ptr(), v.data_ptr(), scales.data_ptr(), *k.stride()[:3], *v.stride()[:3], *k.shape, page // n)
+        self._ref, self._index = _byref(self.args), k.get_device()
+
+    def _append(self):
+        return lib().sgemv_append8, "sgemv_append8"
+
+    def _attend(self, window, sinks):
+        L = lib()
+        return L.sgemv_attend8_plan, L.sgemv_attend8, (window, sinks), "sgemv_attend8"
 
 
 def adjust_logits(x, out=None, history=None, history_start=None, prompt_len=None, repetition=None, frequency=None,
@@ -435,4 +518,49 @@ def adjust_logits(x, out=None, history=None, history_start=None, prompt_len=None
         _leave(ctx)
     if code:
         _check(code, "sgemv_adjust_logits")
+    return out
+
+
+def sample(x, uniform, temperature=None, top_k=None, top_p=None, min_p=None, out=None, logprob=None, stream=None):
+    """A token for each row of logits x [rows, vocab] (FP16, BF16 or FP32): int32 [rows].
+
+    uniform (float32 [rows]): random numbers in [0, 1), the only source of
+    chance. Of a row's tokens, whose p is exp((x - max) / temperature), those of
+    ``min_p`` and more are kept, of these the ``top_k`` largest, of these the
+    fewest largest that sum to ``top_p`` of them; equal logits count by id. The
+    token is the first by id up to which the kept p sum to more than uniform
+    times their sum. temperature, top_p, min_p: float32 [rows]; top_k: int32
+    [rows]; temperature 0 or less takes the largest logit, top_k 0 or less, top_p
+    1 or more and min_p 0 or less leave all. out (int32 [rows]): the tokens;
+    logprob (float32 [rows]): the logarithm of each one's share of what is kept.
+    A row of -inf and NaN alone gets -1 and -inf."""
+    if torch is None:
+        _init()
+    dev, card = x.device, x.get_device()
+    if x.dim() != 2 or (x.stride(1) != 1 and x.shape[1] > 1):
+        raise ValueError("x must be [rows, vocab] with contiguous rows")
+    rows, vocab = x.shape
+    one, f32, i32 = (rows,), torch.float32, torch.int32
+
+    def at(t, what, dtype):
+        if t is None:
+            return 0
+        if t.dtype != dtype or t.shape != one or not t.is_contiguous() or t.get_device() != card:
+            raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {list(one)} on {dev}")
+        return t.data_ptr()
+
+    u = at(uniform, "uniform", f32)
+    rest = at(temperature, "temperature", f32), at(top_k, "top_k", i32), at(top_p, "top_p", f32), at(min_p, "min_p", f32)
+    ids, lp = at(out, "out", i32), at(logprob, "logprob", f32)
+    dtype = _type(x.dtype)
+    s, ctx = _enter(dev, stream)
+    try:
+        if out is None:
+            out = torch.empty(one, dtype=i32, device=dev)
+            ids = out.data_ptr()
+        code = lib().sgemv_sample(_pack_sampling(x.data_ptr(), x.stride(0), u, *rest, ids, lp, rows, vocab, dtype), s)
+    finally:
+        _leave(ctx)
+    if code:
+        _check(code, "sgemv_sample")
     return out

@@ -119,7 +119,13 @@ def lib():
             "sgemv_append": [P, P, P, P, P, P, P, P, P],
             "sgemv_attend_plan": [P, P, i32, i32, i32, P],
             "sgemv_attend": [P, P, P, P, f32, P, i32, i32, P, i64, P],
+            "sgemv_attend_window_plan": [P, P, i32, i32, i32, i32, i32, P],
+            "sgemv_attend_window": [P, P, P, P, f32, P, i32, i32, i32, i32, P, i64, P],
+            "sgemv_append8": [P, P, P, P, P, P, P, P, P],
+            "sgemv_attend8_plan": [P, P, i32, i32, i32, i32, i32, P],
+            "sgemv_attend8": [P, P, P, P, f32, P, i32, i32, i32, i32, P, i64, P],
             "sgemv_adjust_logits": [P, P],
+            "sgemv_sample": [P, P],
         }
         for f, argtypes in sigs.items():
             if not hasattr(L, f):

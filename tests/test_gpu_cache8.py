@@ -1,0 +1,405 @@
+"""GPU parity of the cache in 8 bits and of attention through a window against
+their FP64 oracle.
+
+Tolerances count roundings as those of the 16-bit operators do (u the type's half
+step, e = 2^-24):
+
+* append: without rotary positions the codes and scales are the oracle's, bit
+  for bit. With them a turned value is off by t = 2^-20 m (|x| + |y|) (counted
+  with the 16-bit append), so its code may be that of a value t away: the decoded
+  value is off by half a step of e4m3 there, 2^-4 (|ref| + t) or 2^-10 of the
+  scale for subnormals, and t. A scale may differ where the largest value lies
+  within t of a border.
+* attention: the 16-bit attention's bound, on the values that codes and scales
+  stand for.
+"""
+import numpy as np
+import pytest
+
+import sparse_weight_only_amd as sg
+from gpu_util import say
+from oracle import decode as odec
+from test_gpu_decode import A, ATTEND, BF16, E, F16, TREE, U, Setup, host, ints, name
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    sg.lib()
+
+
+def raw(x):
+    return x.contiguous().view(torch.uint8).cpu().numpy()
+
+
+class Setup8(Setup):
+    """A Setup over a cache in 8 bits: random codes, a scale for each block and head."""
+
+    def __init__(self, n, ctx, page, heads, kv, dim, dtype, seed=0, lead=0, trail=0, head_major=False, spare=2, per_seq=None, block=8,
+                 spread=3):
+        super().__init__(n, ctx, page, heads, kv, dim, dtype, seed, lead, trail, False, spare, per_seq)
+        g = torch.Generator(device="cuda").manual_seed(seed + 1000)
+        self.block = min(block, page)
+        def codes():
+            x = (100.0 * torch.randn(self.n_pages, page, kv, dim, device="cuda", generator=g)).clamp(-448, 448).to(torch.float8_e4m3fn)
+            return x.transpose(1, 2).contiguous().transpose(1, 2) if head_major else x
+        self.k8, self.v8 = codes(), codes()
+        s = torch.randint(120 - spread, 121, (self.n_pages, page // self.block, kv, 2), device="cuda", generator=g)
+        self.scales = s.to(torch.uint8).view(torch.float8_e8m0fnu)
+        self.cache = sg.PagedCache8.from_tensors(self.k8, self.v8, self.scales)
+        self.values()
+
+    def values(self):
+        """The cache's values, for the oracle and the tolerance, as they are now."""
+        k, v, s = raw(self.k8).reshape(self.k8.shape), raw(self.v8).reshape(self.v8.shape), raw(self.scales)
+        self.kc, self.vc = (torch.from_numpy(odec.values8(c, s, i)) for i, c in enumerate((k, v)))
+
+    def want(self, scale=None, tree=None, window=0, sinks=0):
+        return odec.attend(host(self.q), host(self.kc), host(self.vc), self.new_start, self.ctx, self.pages,
+                           scale or self.dim ** -0.5, tree, window, sinks)
+
+
+# ---------------------------------------------------------------- append
+
+APPEND = [
+    # n, ctx, page, block, heads, kv, dim, rot, interleaved, dtype, lead, trail
+    ([1], [1], 8, 8, 1, 1, 16, 16, False, F16, 0, 0),
+    ([1], [700], 16, 16, 32, 32, 128, 128, False, F16, 0, 0),
+    ([3, 0, 5, 1], [3, 7, 60, 33], 16, 8, 4, 2, 64, 64, True, BF16, 0, 0),
+    ([2, 9], [30, 9], 8, 8, 5, 5, 80, 20, False, F16, 1, 2),
+    ([4, 40], [100, 45], 32, 32, 6, 3, 96, 24, True, BF16, 2, 1),
+    ([1] * 70, list(range(1, 71)), 64, 32, 8, 1, 128, 96, False, F16, 0, 0),
+    ([17], [17], 8, 8, 3, 3, 256, 2, False, BF16, 0, 3),
+    ([400], [1000], 256, 128, 2, 1, 256, 256, True, F16, 0, 0),          # every lane of a workgroup, and its most sines
+    ([130, 64], [135, 200], 128, 128, 3, 2, 128, 64, False, BF16, 0, 0),
+    ([777], [777], 64, 64, 3, 2, 64, 64, False, F16, 1, 0),
+    ([33, 1], [50, 17], 16, 16, 2, 2, 48, 48, False, F16, 0, 0),
+]
+
+
+def check_append(s, before, rope_args, q0, out, x_k, x_v, pos):
+    """The cache, its scales and q after an append, against the oracle; x_k and x_v FP64 as stored, pos by row."""
+    turns, inter, m = rope_args
+    of = odec.slots(s.new_start, s.ctx)
+    mine = np.array([r in of for r in range(s.tokens)])
+    def slack(x):
+        half = 0 if turns is None else len(turns)
+        t = np.zeros(x.shape)
+        if half:
+            i0, i1 = (np.arange(half) * 2, np.arange(half) * 2 + 1) if inter else (np.arange(half), np.arange(half) + half)
+            both = np.abs(x[..., i0]) + np.abs(x[..., i1])
+            t[..., i0] = t[..., i1] = 2.0 ** -20 * m * both
+        return t
+    if out is not None:
+        ref = odec.rope(q0, pos, turns, inter, m)
+        ok = np.abs(host(out) - ref) <= slack(q0) + U[s.dtype] * np.abs(ref) + A[s.dtype]
+        assert ok[mine].all()
+        assert np.array_equal(host(out)[~mine], q0[~mine]) or (host(out)[~mine] == 77.0).all(), "a row of no sequence was written"
+    k0, v0, s0 = before
+    v_ref, s_ref = odec.append8(v0, s0, x_v, 1, s.new_start, s.ctx, s.pages)
+    k_ref, s_ref = odec.append8(k0, s_ref, x_k if turns is None else odec.rope(x_k, pos, turns, inter, m), 0, s.new_start, s.ctx, s.pages)
+    got_k, got_v, got_s = (raw(t).reshape(t.shape) for t in (s.k8, s.v8, s.scales))
+    assert np.array_equal(got_v, v_ref) and np.array_equal(got_s[..., 1], s_ref[..., 1]), "V"
+    if turns is None:
+        assert np.array_equal(got_k, k_ref) and np.array_equal(got_s[..., 0], s_ref[..., 0]), "K"
+        return
+    # a border within the slack would be a coincidence of 2^-18 or so for each block: none in these cases
+    assert np.array_equal(got_s[..., 0], s_ref[..., 0]), "scales of K"
+    a, b = odec.values8(got_k, got_s, 0), odec.values8(k_ref, s_ref, 0)
+    step = 2.0 ** (np.repeat(s_ref[..., 0].astype(int), s.block, 1) - 127)[..., None]
+    near = np.abs(a - b) <= 2.0 ** -3 * np.abs(b) + 2.0 ** -9 * step
+    assert near.all(), "codes of K more than one apart"
+    # each new code is a nearest one of a value within the slack
+    each = s.page
+    for row, (q, _, slot) in of.items():
+        if slot < 0 or slot // each >= s.pages.shape[1] or not 0 <= s.pages[q, slot // each] < s.n_pages:
+            continue
+        at = int(s.pages[q, slot // each]), slot % each
+        ref, t = odec.rope(x_k[row:row + 1], [pos[row]], turns, inter, m)[0], slack(x_k[row:row + 1])[0]
+        far = np.abs(a[at] - ref) - (t + np.maximum(2.0 ** -4 * (np.abs(ref) + t), 2.0 ** -10 * step[at]))
+        assert (far <= 0).all(), (row, far.max())
+    new = np.zeros(got_k.shape[:2], bool)
+    for _, (q, _, slot) in of.items():
+        if slot >= 0 and slot // each < s.pages.shape[1] and 0 <= s.pages[q, slot // each] < s.n_pages:
+            new[s.pages[q, slot // each], slot % each] = True
+    assert np.array_equal(got_k[~new], k_ref[~new]), "older codes"
+
+
+def state(s):
+    return tuple(raw(t).reshape(t.shape) for t in (s.k8, s.v8, s.scales))
+
+
+@pytest.mark.parametrize("case", APPEND, ids=lambda c: f"n{len(c[0])}x{max(c[0])}_b{c[3]}_d{c[6]}_r{c[7]}_{'i' if c[8] else 'h'}")
+@pytest.mark.parametrize("how", ["plain", "rope", "in place"])
+def test_append8(case, how):
+    n, ctx, page, block, heads, kv, dim, rot, inter, dtype, lead, trail = case
+    say("case append8", case, how)
+    s = Setup8(n, ctx, page, heads, kv, dim, dtype, 1, lead, trail, block=block, spread=6)
+    # magnitudes that call for scales above and below the older ones
+    s.v *= torch.exp2(torch.randint(-6, 7, (s.tokens, kv, 1), device="cuda").float()).to(dtype)
+    of = odec.slots(s.new_start, ctx)
+    pos = [of[r][2] if r in of else 0 for r in range(s.tokens)]
+    before = state(s)
+    k, v, q0 = host(s.k), host(s.v), host(s.q)
+    if how == "plain":
+        assert s.cache.append(s.seqs, s.k, s.v) is None
+        check_append(s, before, (None, False, 1.0), None, None, k, v, pos)
+        return
+    rope = sg.Rope(rot, interleaved=inter, magnitude=1.25)
+    out = s.q if how == "in place" else torch.full_like(s.q, 77.0)
+    s.cache.append(s.seqs, s.k, s.v, rope=rope, q=s.q, q_out=out)
+    check_append(s, before, (odec.rope_turns(rot), inter, 1.25), q0, out, k, v, pos)
+
+
+def test_append8_token_by_token():
+    """Block by block, tokens whose magnitudes rise and fall: scales grow with them and start anew with a block."""
+    say("case append8 token by token")
+    s = Setup8([1, 1], [1, 1], 16, 2, 2, 32, F16, 2, per_seq=4, spare=10, block=16)
+    s.pages[:] = [[0, 1, 2, 3], [4, 5, 6, 7]]
+    s.seqs.pages.copy_(ints(s.pages))
+    rng = np.random.default_rng(3)
+    for step in range(50):
+        s.ctx = [step + 1, min(step + 7, 64)]
+        s.seqs.ctx_len.copy_(ints(s.ctx))
+        for t in (s.k, s.v):
+            t.copy_(torch.from_numpy(rng.standard_normal(t.shape) * 2.0 ** rng.integers(-12, 8)).half())
+        before = state(s)
+        s.cache.append(s.seqs, s.k, s.v)
+        check_append(s, before, (None, False, 1.0), None, None, host(s.k), host(s.v), None)
+    assert len(set(raw(s.scales)[..., 0].reshape(-1).tolist())) > 4
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_append8_special_values(dtype):
+    say("case append8 special values", dtype)
+    s = Setup8([9], [12], 16, 2, 2, 16, dtype, 4, block=8)
+    big = torch.finfo(dtype).max
+    s.k.zero_()
+    s.v[0], s.v[1, 0, 0], s.v[1, 0, 1], s.v[1, 1, 2] = 0.0, float("inf"), float("nan"), -float("inf")
+    s.v[2, 0, 3], s.v[6:, 1] = big, torch.finfo(dtype).tiny
+    s.k[7] = -0.0
+    before = state(s)
+    s.cache.append(s.seqs, s.k, s.v)
+    check_append(s, before, (None, False, 1.0), None, None, host(s.k), host(s.v), None)
+    assert (raw(s.v8).reshape(s.v8.shape)[s.pages[0, 0], 4, 0, :2] & 127 == 127).all()
+
+
+def test_append8_where_nothing_is_stored():
+    """Pages that are not there, and slots below 0: q is turned all the same."""
+    say("case append8 pages not there")
+    s = Setup8([12, 9, 3], [40, 5, 3], 16, 4, 2, 64, F16, 5, block=16)
+    s.pages[0, 1], s.pages[2, 0] = -1, s.n_pages
+    s.seqs.pages.copy_(ints(s.pages))
+    of = odec.slots(s.new_start, s.ctx)
+    pos = [of[r][2] if r in of else 0 for r in range(s.tokens)]
+    before, q0 = state(s), host(s.q)
+    out = s.cache.append(s.seqs, s.k, s.v, rope=sg.Rope(64), q=s.q)
+    check_append(s, before, (odec.rope_turns(64), False, 1.0), q0, out, host(s.k), host(s.v), pos)
+
+
+def test_append8_strided_and_positions():
+    say("case append8 strided")
+    heads, kv, dim = 6, 2, 64
+    s = Setup8([5, 2], [40, 2], 16, heads, kv, dim, BF16, 6, head_major=True, block=8)
+    qkv = torch.randn(s.tokens, heads + 2 * kv, dim, device="cuda").to(BF16)
+    s.q, s.k, s.v = qkv[:, :heads], qkv[:, heads: heads + kv], qkv[:, heads + kv:]
+    pos = [1000000, -7, 3, 3, 2 ** 31 - 1, 0, 77]
+    before, q0 = state(s), host(s.q)
+    out = s.cache.append(s.seqs, s.k, s.v, rope=sg.Rope(32), q=s.q, positions=ints(pos))
+    check_append(s, before, (odec.rope_turns(32), False, 1.0), q0, out, host(s.k), host(s.v), pos)
+
+
+def test_append8_far_into_a_large_cache():
+    """Offsets beyond 2^32 bytes."""
+    say("case append8 far")
+    page, kv, dim = 16, 2, 64
+    pages = (1 << 32) // (page * kv * dim) + 3
+    k, v = (torch.zeros(pages, page, kv, dim, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2))
+    cache = sg.PagedCache8.from_tensors(k, v, torch.full((pages, 1, kv, 2), 31, dtype=torch.uint8, device="cuda").view(torch.float8_e8m0fnu))
+    x = torch.randn(3, kv, dim, device="cuda").half()
+    seqs = sg.Sequences(ints([0, 3]), ints([3]), ints([[pages - 1]]))
+    cache.append(seqs, x, -x)
+    got = odec.values8(raw(k[-1:]).reshape(1, page, kv, dim), raw(cache.scales[-1:]), 0)[0, :3]
+    top = 2.0 ** (raw(cache.scales[-1:])[0, 0, :, 0].astype(int) - 127)
+    assert (np.abs(got - host(x)) <= np.maximum(2.0 ** -4 * np.abs(host(x)), 2.0 ** -10 * top[None, :, None])).all()
+    assert not k.view(torch.uint8)[0].any()
+    q = torch.randn(3, kv, dim, device="cuda").half()
+    out = cache.attend(seqs, q, window=2)
+    vals = [odec.values8(raw(t[-1:]).reshape(1, page, kv, dim), raw(cache.scales[-1:]), i) for i, t in enumerate((k, v))]
+    ref, mean, worst, keys = odec.attend(host(q), *vals, [0, 3], [3], np.array([[0]]), dim ** -0.5, window=2)
+    tol = mean * (3 * U[F16] + 2 * dim * E * worst[:, :, None] + 2 * keys[:, :, None] * E) + 3 * A[F16] * np.abs(vals[1]).max() + A[F16]
+    assert (np.abs(host(out) - ref) <= tol).all()
+
+
+# ------------------------------------------------------------- attention
+
+def fits(case):
+    return case[5] % 16 == 0
+
+
+@pytest.mark.parametrize("case", [c for c in ATTEND if fits(c)], ids=name)
+@pytest.mark.parametrize("block", [8, 32])
+def test_attend8(case, block):
+    n, ctx, page, heads, kv, dim, dtype, lead, trail, head_major, max_ctx = case
+    say("case attend8", case, block)
+    s = Setup8(n, ctx, page, heads, kv, dim, dtype, 5, lead, trail, head_major, block=block)
+    want = s.want()
+    out = torch.full_like(s.q, 55.0)
+    assert s.cache.attend(s.seqs, s.q, out=out, max_ctx=max_ctx) is out
+    s.check(out, want, name(case))
+    mine = ~np.isnan(want[0][:, 0, 0])
+    assert (host(out)[~mine] == 55.0).all(), "a row of no sequence was written"
+    again = s.cache.attend(s.seqs, s.q, max_ctx=max_ctx)
+    assert torch.equal(again[torch.from_numpy(mine)], out[torch.from_numpy(mine)]), "not the same bits twice"
+
+
+WINDOW = [(1, 0), (7, 3), (64, 0), (100, 40), (33, 500), (2 ** 31 - 1, 5)]
+
+
+@pytest.mark.parametrize("case", [c for c in ATTEND if fits(c)][::2] + [ATTEND[1]], ids=name)
+@pytest.mark.parametrize("window,sinks", WINDOW)
+@pytest.mark.parametrize("kind", [Setup, Setup8])
+def test_attend_window(case, window, sinks, kind):
+    n, ctx, page, heads, kv, dim, dtype, lead, trail, head_major, max_ctx = case
+    say("case window", case, window, sinks, kind.__name__)
+    s = kind(n, ctx, page, heads, kv, dim, dtype, 6, lead, trail, head_major)
+    want = odec.attend(host(s.q), host(s.kc), host(s.vc), s.new_start, s.ctx, s.pages, dim ** -0.5, None, window, sinks)
+    out = torch.full_like(s.q, 55.0)
+    s.cache.attend(s.seqs, s.q, out=out, max_ctx=max_ctx, window=window, sinks=sinks)
+    s.check(out, want, name(case))
+    mine = ~np.isnan(want[0][:, 0, 0])
+    assert (host(out)[~mine] == 55.0).all(), "a row of no sequence was written"
+
+
+@pytest.mark.parametrize("n,ctx", TREE)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (3, 2), (40, 0), (300, 70)])
+@pytest.mark.parametrize("kind", [Setup, Setup8])
+def test_attend_tree_window(n, ctx, window, sinks, kind):
+    say("case tree window", n, ctx, window, sinks, kind.__name__)
+    dim, heads, kv = (128, 4, 2) if len(n) % 2 else (64, 3, 3)
+    s = kind(n, ctx, 16, heads, kv, dim, F16, 7)
+    rng = np.random.default_rng(8)
+    words = (max(n) + 31) // 32 + 1
+    bits = np.zeros((s.tokens, words), np.uint32)
+    for q in range(len(n)):
+        for i in range(n[q]):
+            up, j = {i}, i
+            while j:
+                j = (j - 1) // 2
+                up.add(j)
+            if i % 5 == 4:
+                up = set(np.flatnonzero(rng.random(n[q]) < 0.3).tolist())
+            for j in up:
+                bits[s.new_start[q] + i, j // 32] |= np.uint32(1) << np.uint32(j % 32)
+    want = odec.attend(host(s.q), host(s.kc), host(s.vc), s.new_start, s.ctx, s.pages, dim ** -0.5, bits, window, sinks)
+    got = s.cache.attend(s.seqs, s.q, tree=ints(bits.view(np.int32)), window=window, sinks=sinks)
+    s.check(got, want, f"tree {n} {ctx} {window} {sinks}")
+
+
+@pytest.mark.parametrize("n,ctx,heads,kv", [([1], [300], 2, 2), ([3], [1500], 4, 2), ([60], [200], 2, 1), ([90], [1200], 4, 2), ([300], [700], 1, 1)])
+def test_attend8_unseen_slots_have_no_part(n, ctx, heads, kv):
+    """NaN codes behind the end and outside the window, and any scales in blocks that no token sees."""
+    say("case attend8 unseen", n, ctx)
+    s = Setup8(n, ctx, 16, heads, kv, 64, F16, 9, spare=3)
+    first = ctx[0] - n[0]
+    window, sinks = 50, 9
+    got = s.cache.attend(s.seqs, s.q, window=window, sinks=sinks)
+    plain = s.cache.attend(s.seqs, s.q)
+    bad = np.zeros((s.n_pages, 16), bool)
+    block = np.zeros((s.n_pages, 2), bool)
+    bad[s.unused], block[s.unused] = True, True
+    low = first + 1 - window
+    for t in range(s.pages.shape[1] * 16):
+        at = s.pages[0, t // 16], t % 16
+        if t >= ctx[0] or sinks <= t < low:
+            bad[at] = True
+    hidden = bad.reshape(s.n_pages, 2, 8).all(2)
+    for c in (s.k8, s.v8):
+        c.view(torch.uint8)[torch.from_numpy(bad).cuda()] = 0x7F
+    for e in (0, 254, 255):
+        s.scales.view(torch.uint8)[torch.from_numpy(hidden).cuda()] = e
+        again = s.cache.attend(s.seqs, s.q, window=window, sinks=sinks)
+        assert not torch.isnan(again).any()
+        want = odec.attend(host(s.q), np.nan_to_num(host(s.kc)), np.nan_to_num(host(s.vc)), s.new_start, s.ctx, s.pages, 0.125, None, window, sinks)
+        s.check(again, want, f"scales of {e}")
+    # pages out of the window may be given back
+    gone = [i for i in range(s.pages.shape[1]) if 16 * i >= sinks and 16 * (i + 1) <= low]
+    pages = s.pages.copy()
+    pages[0, gone] = -1
+    s.seqs.pages.copy_(ints(pages))
+    assert torch.equal(s.cache.attend(s.seqs, s.q, window=window, sinks=sinks), again)
+    assert not torch.isnan(got).any() and not torch.isnan(plain).any()
+
+
+@pytest.mark.parametrize("n,ctx", [([1], [40]), ([20], [300]), ([150], [400])])
+def test_attend8_nan_that_is_seen(n, ctx):
+    say("case attend8 NaN", n, ctx)
+    s = Setup8(n, ctx, 16, 2, 1, 64, F16, 10)
+    s.v8.view(torch.uint8)[s.pages[0, 1], 3, 0, 5] = 0x7F
+    got = host(s.cache.attend(s.seqs, s.q))
+    assert np.isnan(got[:, :, 5]).all() and not np.isnan(np.delete(got, 5, 2)).any()
+
+
+@pytest.mark.parametrize("n,ctx,dim", [([1], [700], 128), ([30], [300], 64), ([90], [1300], 128), ([300], [500], 256), ([260], [400], 64)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("far", [14, 17, 45, 90])
+def test_attend8_exponents_far_apart(n, ctx, dim, dtype, far):
+    """Rows that see only blocks of small scales beside rows that see large ones."""
+    say("case attend8 far exponents", n, ctx, dim, dtype, far)
+    s = Setup8(n, ctx, 16, 2, 1, dim, dtype, 11, block=8)
+    e = torch.full((s.n_pages, 2, 1, 2), 120 - far // 2, dtype=torch.uint8, device="cuda")
+    up = 120 + (far + 1) // 2 if dtype == BF16 else 122
+    e[..., 0] = 120
+    if dtype == F16:
+        e[..., 1] = up - min(far, 24)
+    late = ctx[0] - n[0] // 2
+    e[s.pages[0, late // 16], late % 16 // 8, 0, 1] = up        # seen by the last rows alone (or by the only one)
+    e[s.pages[0, 0], 0, 0, 0] = 120 - min(far, 50)
+    s.scales.view(torch.uint8).copy_(e)
+    s.values()
+    want = s.want()
+    out, mean, worst, keys = want
+    got = host(s.cache.attend(s.seqs, s.q))
+    u, a = U[dtype], A[dtype]
+    # half subnormals of the weights count by what the row itself sees: as those sums have them, n a max |v| of the row
+    old = ctx[0] - n[0]
+    big = np.array([max(np.abs(host(s.vc)[s.pages[0, t // 16], t % 16]).max() for t in (range(old + i + 1) if i % 7 == 0 or i == n[0] - 1 else [old + i]))
+                    for i in range(n[0])])
+    for i in range(n[0]):
+        if not (i % 7 == 0 or i == n[0] - 1):
+            continue
+        tol = mean[i] * (3 * u + 2 * dim * E * worst[i][:, None] + 2 * keys[i][:, None] * E) + keys[i][:, None] * a * big[i] + a
+        assert (np.abs(got[i] - out[i]) <= tol).all(), (i, (np.abs(got[i] - out[i]) - tol).max())
+
+
+def test_attend8_lengths_that_do_not_fit():
+    say("case attend8 lengths")
+    s = Setup8([3, 40], [50, 60], 16, 2, 1, 64, F16, 12, per_seq=4, spare=12)
+    s.seqs.ctx_len.copy_(ints([10 ** 9, -5]))
+    s.ctx = [10 ** 9, -5]
+    for window, sinks in ((0, 0), (20, 3)):
+        got = host(s.cache.attend(s.seqs, s.q, window=window, sinks=sinks))
+        assert (got[3:] == 0).all() and np.isfinite(got[:3]).all()
+
+
+def test_streams_and_workspace():
+    say("case streams 8")
+    a = Setup8([1, 1], [3000, 900], 16, 8, 2, 128, F16, 17)
+    b = Setup8([70], [700], 16, 4, 2, 64, BF16, 18)
+    wa, wb = a.cache.attend(a.seqs, a.q), b.cache.attend(b.seqs, b.q, window=90, sinks=3)
+    room = torch.empty(a.cache.plan(a.seqs, 2, 8).workspace_bytes, dtype=torch.uint8, device="cuda")
+    assert room.numel() > 0
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(8):
+        got.append((a.cache.attend(a.seqs, a.q, stream=s1, workspace=room), b.cache.attend(b.seqs, b.q, stream=s2, window=90, sinks=3)))
+    s1.synchronize()
+    s2.synchronize()
+    assert all(torch.equal(x, wa) and torch.equal(y, wb) for x, y in got)
+    with pytest.raises(sg.SgemvError):
+        a.cache.attend(a.seqs, a.q, workspace=room[:-8])
