@@ -19,8 +19,8 @@ using sgemv_dev::SeqView;
 using sgemv_dev::dword2;
 using sgemv_dev::dword4;
 
-constexpr int kLanes = 256;
-constexpr int kHold = 16;                    // tokens of a lane
+constexpr int kMostLanes = 1024;              // of a workgroup: 256 columns and 128 new tokens
+constexpr int kHold = 4;                     // tokens of a lane
 constexpr int kLeast = 127 - 96, kMost = 127 + 120;
 
 struct RowsView {
@@ -44,7 +44,7 @@ struct Append8Params {
   int32_t rot, interleaved;
   int32_t block_shift;                       // log2 of B
   int32_t sines;                             // angles that a block may need
-  int32_t per, groups;                       // heads of a workgroup; lanes that share a head's tokens
+  int32_t lanes, per, groups;                // of a workgroup: lanes, heads; lanes that share a head's tokens
 };
 
 template <class T>
@@ -59,8 +59,8 @@ __device__ __forceinline__ int exponent_of(uint32_t a) {
   return e < kLeast ? kLeast : e > kMost ? kMost : e;
 }
 
-// 8 values as codes of the biased exponent e.
-__device__ __forceinline__ dword2 codes_of(const float (&v)[8], int e) {
+// 8 values as codes of the biased exponent e. `odd`: some are not finite.
+__device__ __forceinline__ dword2 codes_of(const float (&v)[8], int e, bool odd) {
   uint32_t w[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -69,18 +69,25 @@ __device__ __forceinline__ dword2 codes_of(const float (&v)[8], int e) {
     for (int k = 0; k < 4; ++k) y[k] = __builtin_amdgcn_ldexpf(v[4 * i + k], 127 - e);
     int u = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
     u = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], u, true);
+    if (odd) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (!(__builtin_fabsf(v[4 * i + k]) < __builtin_inff())) u = (u & ~(0xff << 8 * k)) | 0x7f << 8 * k;
+      for (int k = 0; k < 4; ++k)
+        if (!(__builtin_fabsf(v[4 * i + k]) < __builtin_inff())) u = (u & ~(0xff << 8 * k)) | 0x7f << 8 * k;
+    }
     w[i] = (uint32_t)u;
   }
   return dword2{w[0], w[1]};
 }
 
+// How a chunk of 8 columns finds the others of its pairs: in a chunk of its own
+// (halves of a multiple of 8 columns), within itself (interleaved, in whole
+// chunks), or column by column.
+enum Pairing { kApart, kWithin, kAnyhow };
+
 // Workgroup (u, y): block u of those that new tokens fall into, heads y per ...
 // of the list q0 .. q(nq-1), k0 .. k(nkv-1), v0 .. v(nkv-1); q goes along, its
 // tokens being those of the block's slots. A lane has one chunk of 8 columns of
-// one head in up to 16 of the block's tokens, from the load to the store, so
+// one head in up to 4 of the block's tokens, from the load to the store, so
 // that every row is read once: the values stay in registers while the block's
 // largest magnitude is found in LDS. A rotated chunk reads its partner's columns
 // beside its own (from the same cache lines as the lane that has them).
@@ -89,8 +96,8 @@ __device__ __forceinline__ dword2 codes_of(const float (&v)[8], int e) {
 // Blocks are numbered without a pass over the sequences: sequence s, whose
 // first new token is a, has the numbers from floor(a / B) + 2 s on; n tokens fall
 // into at most floor(n / B) + 2 blocks. What is left over is empty.
-template <class T>
-__global__ void __launch_bounds__(kLanes) append8_kernel(Append8Params p) {
+template <class T, Pairing PAIRING>
+__global__ void __launch_bounds__(kMostLanes) append8_kernel(Append8Params p) {
   extern __shared__ float2 trig[];                         // [token of the block][pair], then
   uint32_t* top = (uint32_t*)(trig + p.sines);             // [head] the largest magnitude
   const int tid = threadIdx.x, unit = blockIdx.x;
@@ -136,63 +143,81 @@ __global__ void __launch_bounds__(kLanes) append8_kernel(Append8Params p) {
   {
     const RowsView& src = is_q ? p.q : is_k ? p.k : p.v;
     const uint16_t* from = src.p + hh * src.head;
-    // the chunk's partners: another chunk, its own columns, or anything
-    const bool apart = turned && !p.interleaved && pairs % 8 == 0, odd = turned && !p.interleaved && pairs % 8 != 0;
     const int partner = first < pairs ? first + pairs : first - pairs;
-    dword4 own[kHold], other[kHold];
+    dword4 own[kHold], other[PAIRING == kWithin ? 1 : kHold];
 #pragma unroll
     for (int j = 0; j < kHold; ++j) {
       const int at = j * p.groups + group;
       own[j] = dword4{0, 0, 0, 0};
-      other[j] = dword4{0, 0, 0, 0};
+      if (PAIRING != kWithin) other[j] = dword4{0, 0, 0, 0};
       if (j * p.groups >= n) break;
       if (!work || at >= n) continue;
       const uint16_t* row = from + (int64_t)(tok0 + at) * src.token;
       own[j] = *(const dword4*)(row + first);
-      if (apart) other[j] = *(const dword4*)(row + partner);
-      if (odd) {
+      if (PAIRING == kApart && turned) other[j] = *(const dword4*)(row + partner);
+      if (PAIRING == kAnyhow && turned) {
         uint16_t y[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int d = first + e;
-          y[e] = d < p.rot ? row[d < pairs ? d + pairs : d - pairs] : 0;
+          y[e] = d < p.rot ? row[p.interleaved ? d ^ 1 : d < pairs ? d + pairs : d - pairs] : 0;
         }
         other[j] = *(const dword4*)y;
       }
     }
-    if (p.rot > 0) {
-      for (int i = tid; i < n * pairs; i += kLanes) {
-        const int at = i / pairs, j = i - at * pairs;
+    if (p.rot > 0 && tid < p.lanes / pairs * pairs) {
+      const int j = tid % pairs;
+      const double turns = p.turns[j];
+      for (int at = tid / pairs; at < n; at += p.lanes / pairs) {
         const int pos = p.positions ? p.positions[tok0 + at] : lo + at;
-        const double rev = (double)pos * p.turns[j];
+        const double rev = (double)pos * turns;
         float sn, cs;
         sincospif(2.0f * (float)(rev - rint(rev)), &sn, &cs);
-        trig[i] = float2{cs * p.magnitude, sn * p.magnitude};
+        trig[at * pairs + j] = float2{cs * p.magnitude, sn * p.magnitude};
       }
     }
     top[tid] = 0;
     // every row has been read, by every lane, before any is written (q_out may be q)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
+    const bool low = first < pairs;                        // kApart: of the whole chunk
+    const float sign = low ? -1.0f : 1.0f;
 #pragma unroll
     for (int j = 0; j < kHold; ++j) {
       const int at = j * p.groups + group;
       if (j * p.groups >= n) break;
       uint16_t u[8], w[8];
       *(dword4*)u = own[j];
-      *(dword4*)w = other[j];
+      if (PAIRING != kWithin) *(dword4*)w = other[j];
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[j][e] = to_f<T>(u[e]);
       if (!turned || at >= n) continue;
       const float2* t = trig + at * pairs;
+      if (PAIRING == kApart) {
+        t += low ? first : first - pairs;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int d = first + e;
-        if (d >= p.rot) continue;
-        const bool low = p.interleaved ? !(d & 1) : d < pairs;
-        const float2 c = t[p.interleaved ? d >> 1 : low ? d : d - pairs];
-        const float own_e = to_f<T>(u[e]), other_e = to_f<T>(p.interleaved ? u[e ^ 1] : w[e]);
-        x[j][e] = low ? own_e * c.x - other_e * c.y : other_e * c.y + own_e * c.x;
+        for (int e = 0; e < 8; ++e) {
+          const float2 c = t[e];
+          x[j][e] = x[j][e] * c.x + to_f<T>(w[e]) * (sign * c.y);
+        }
+      } else if (PAIRING == kWithin) {
+        t += first / 2;
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          const float2 c = t[e / 2];
+          const float a0 = x[j][e], b0 = x[j][e + 1];
+          x[j][e] = a0 * c.x - b0 * c.y;
+          x[j][e + 1] = b0 * c.x + a0 * c.y;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int d = first + e;
+          if (d >= p.rot) continue;
+          const bool one = p.interleaved ? !(d & 1) : d < pairs;
+          const float2 c = t[p.interleaved ? d >> 1 : one ? d : d - pairs];
+          x[j][e] = x[j][e] * c.x + to_f<T>(w[e]) * (one ? -c.y : c.y);
+        }
       }
     }
   }
@@ -216,19 +241,30 @@ __global__ void __launch_bounds__(kLanes) append8_kernel(Append8Params p) {
   const bool write = (is_k || is_v) && store;
   int was = 0;
   if (write && older) was = *scale;
+  bool odd = false;                                        // some of the lane's values are not finite
   if (write) {
-    uint32_t most = 0;
+    float most = 0.0f, none = 0.0f;
 #pragma unroll
     for (int j = 0; j < kHold; ++j) {
       if (j * p.groups >= n) break;
-      if (j * p.groups + group >= n) continue;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const uint32_t m = __builtin_bit_cast(uint32_t, x[j][e]) & 0x7fffffffu;
-        most = m < 0x7f800000u && m > most ? m : most;
+        most = fmaxf(most, __builtin_fabsf(x[j][e]));
+        none = __builtin_fmaf(x[j][e], 0.0f, none);        // not a number after one that is not finite
       }
     }
-    atomicMax(&top[mine], most);
+    odd = none != 0.0f;
+    if (odd) {
+      most = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kHold; ++j) {
+        if (j * p.groups >= n) break;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (__builtin_fabsf(x[j][e]) < __builtin_inff()) most = fmaxf(most, __builtin_fabsf(x[j][e]));
+      }
+    }
+    atomicMax(&top[mine], __builtin_bit_cast(uint32_t, most));
   }
   // `was` has been read, by every lane, before it is written
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -258,9 +294,15 @@ __global__ void __launch_bounds__(kLanes) append8_kernel(Append8Params p) {
     const int at = j * p.groups + group;
     if (j * p.groups >= n) break;
     if (at >= n) continue;
-    *(dword2*)(row0 + (older + at) * to.slot) = codes_of(x[j], e);
+    *(dword2*)(row0 + (older + at) * to.slot) = codes_of(x[j], e, odd);
   }
   if (group == 0 && chunk == 0) *scale = (uint8_t)e;
+}
+
+typedef void (*Append8Fn)(Append8Params);
+template <class T>
+Append8Fn pick(Pairing pairing) {
+  return pairing == kApart ? append8_kernel<T, kApart> : pairing == kWithin ? append8_kernel<T, kWithin> : append8_kernel<T, kAnyhow>;
 }
 
 int check_rope(const sgemv_rope_t* r, int dim) {
@@ -327,19 +369,23 @@ extern "C" int sgemv_append8(const sgemv_cache8* cache, const sgemv_seqs* seqs, 
   p.chunks = k->head_dim / 8;
   const int most = B < k->tokens ? B : k->tokens;                // new tokens of a block
   p.groups = (most + kHold - 1) / kHold;
-  const int rooms = kLanes / p.chunks;
-  // 256 columns and 128 tokens fill a workgroup exactly
-  p.per = rooms / p.groups;
+  // four waves, or as many as a head takes (a batch of prompts of up to 4001
+  // tokens, 96 heads of 128 columns, blocks of 16: 149 us with 4 tokens a lane and
+  // 4 waves, 164 with 8 waves; 179 with 2 tokens; 191 with 8, 184 of them and 8 waves)
+  p.lanes = p.chunks * p.groups > 256 ? (p.chunks * p.groups + 63) / 64 * 64 : 256;
+  p.per = p.lanes / p.chunks / p.groups;
   const int64_t units = (k->tokens >> p.block_shift) + 2 * (int64_t)seqs->count;
   const int heads = p.nq + 2 * p.nkv;
-  if (units * kLanes > (int64_t)UINT32_MAX) return SGEMV_ESIZE;  // lanes of a grid axis fit 32 bits
+  if (units * p.lanes > (int64_t)UINT32_MAX) return SGEMV_ESIZE;  // lanes of a grid axis fit 32 bits
   p.sines = most * (p.rot / 2);
-  const int64_t lds = (int64_t)p.sines * 8 + kLanes * 4;
-  const void* fn = k->dtype == SGEMV_F16 ? (const void*)append8_kernel<_Float16> : (const void*)append8_kernel<__bf16>;
+  const int64_t lds = (int64_t)p.sines * 8 + p.lanes * 4;
+  const Pairing pairing = !rope || (!rope->interleaved && rope->rot_dim % 16 == 0) ? kApart
+                          : rope->interleaved && rope->rot_dim % 8 == 0          ? kWithin
+                                                                                 : kAnyhow;
+  const Append8Fn fn = k->dtype == SGEMV_F16 ? pick<_Float16>(pairing) : pick<__bf16>(pairing);
   (void)hipGetLastError();
-  if (ensure_lds(fn, lds)) return SGEMV_EHIP;
+  if (ensure_lds((const void*)fn, lds)) return SGEMV_EHIP;
   const dim3 grid((uint32_t)units, (uint32_t)((heads + p.per - 1) / p.per));
-  if (k->dtype == SGEMV_F16) hipLaunchKernelGGL(append8_kernel<_Float16>, grid, dim3(kLanes), (uint32_t)lds, (hipStream_t)hip_stream, p);
-  else hipLaunchKernelGGL(append8_kernel<__bf16>, grid, dim3(kLanes), (uint32_t)lds, (hipStream_t)hip_stream, p);
+  hipLaunchKernelGGL(fn, grid, dim3(p.lanes), (uint32_t)lds, (hipStream_t)hip_stream, p);
   return hipGetLastError() == hipSuccess ? SGEMV_OK : SGEMV_EHIP;
 }
