@@ -53,22 +53,47 @@ constexpr uint32_t kNever = 0x007fffffu;             // the key of -inf
 // logits the lower id.
 __device__ __forceinline__ uint64_t place_of(uint32_t key, uint32_t id) { return (uint64_t)key << 32 | (uint32_t)~id; }
 
-__device__ __forceinline__ uint64_t shfl64(uint64_t x, int from) {
-  const uint32_t lo = __shfl((uint32_t)x, from), hi = __shfl((uint32_t)(x >> 32), from);
-  return (uint64_t)hi << 32 | lo;
-}
-__device__ __forceinline__ uint64_t wave_prefix(uint64_t x) {   // inclusive
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const uint64_t y = shfl64(x, lane - d);
-    if (lane >= d) x += y;
-  }
+// What a lane gets of x by a data-parallel move (0 where it gets nothing).
+template <int MOVE, int ROWS = 0xf>
+__device__ __forceinline__ uint32_t moved(uint32_t x) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, MOVE, ROWS, 0xf, true); }
+template <int MOVE, int ROWS = 0xf>
+__device__ __forceinline__ uint64_t moved(uint64_t x) { return (uint64_t)moved<MOVE, ROWS>((uint32_t)(x >> 32)) << 32 | moved<MOVE, ROWS>((uint32_t)x); }
+constexpr int kShift1 = 0x111, kShift2 = 0x112, kShift4 = 0x114, kShift8 = 0x118;       // from the lane so many places down, in rows of 16
+constexpr int kLast15 = 0x142, kLast31 = 0x143;                                        // the last lane of the row below, of the lower half
+constexpr int kPair = 0xb1, kQuad = 0x4e, kHalf = 0x141, kMirror = 0x140;              // lanes 1 and 2 away; mirrored in 8, in 16
+
+template <class X>
+__device__ __forceinline__ X wave_prefix(X x) {      // inclusive
+  x += moved<kShift1>(x);
+  x += moved<kShift2>(x);
+  x += moved<kShift4>(x);
+  x += moved<kShift8>(x);
+  x += moved<kLast15, 0xa>(x);
+  x += moved<kLast31, 0xc>(x);
   return x;
 }
-__device__ __forceinline__ uint64_t wave_sum(uint64_t x) {
-#pragma unroll
-  for (int d = 32; d; d /= 2) x += shfl64(x, (threadIdx.x & 63) ^ d);
+__device__ __forceinline__ uint32_t read_lane(uint32_t x, int i) { return (uint32_t)__builtin_amdgcn_readlane((int)x, i); }
+__device__ __forceinline__ uint64_t read_lane(uint64_t x, int i) { return (uint64_t)read_lane((uint32_t)(x >> 32), i) << 32 | read_lane((uint32_t)x, i); }
+template <class X>
+__device__ __forceinline__ X last_lane(X x) { return read_lane(x, 63); }
+__device__ __forceinline__ uint64_t wave_sum(uint64_t x) { return last_lane(wave_prefix(x)); }
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+  const auto up = [&](uint32_t y) { x = y > x ? y : x; };
+  up(moved<kShift1>(x));
+  up(moved<kShift2>(x));
+  up(moved<kShift4>(x));
+  up(moved<kShift8>(x));
+  up(moved<kLast15, 0xa>(x));
+  up(moved<kLast31, 0xc>(x));
+  return last_lane(x);
+}
+// The sum over 4, 8 or 16 neighbouring lanes, in each of them.
+template <class X>
+__device__ __forceinline__ X near_sum(X x, int lanes) {
+  x += moved<kPair>(x);
+  x += moved<kQuad>(x);
+  if (lanes > 4) x += moved<kHalf>(x);
+  if (lanes > 8) x += moved<kMirror>(x);
   return x;
 }
 
@@ -83,46 +108,45 @@ struct Shared {
   uint64_t list[kList];                              // places
   unsigned long long stretch[kWaves];                // sums of the kept p, by waves' stretches of the row
   uint64_t part[kWaves];
-  uint32_t best[kWaves];
+  uint32_t best[2][kWaves];
   uint64_t above, place;
   uint32_t bin_count;
   int bin, listed;
 };
 
-// The largest of a number over the workgroup.
-__device__ __forceinline__ uint32_t block_max(Shared& s, uint32_t v) {
-#pragma unroll
-  for (int d = 32; d; d /= 2) {
-    const uint32_t o = __shfl_xor(v, d);
-    v = o > v ? o : v;
+// The largest of two numbers each over the workgroup.
+__device__ __forceinline__ void block_max(Shared& s, uint32_t& u, uint32_t& v) {
+  u = wave_max(u);
+  v = wave_max(v);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) {
+    s.best[0][threadIdx.x >> 6] = u;
+    s.best[1][threadIdx.x >> 6] = v;
   }
   __syncthreads();
-  if ((threadIdx.x & 63) == 0) s.best[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = s.best[threadIdx.x & (kWaves - 1)];
 #pragma unroll
-  for (int d = kWaves / 2; d; d /= 2) {
-    const uint32_t o = __shfl_xor(v, d);
-    v = o > v ? o : v;
+  for (int w = 0; w < kWaves; ++w) {
+    u = s.best[0][w] > u ? s.best[0][w] : u;
+    v = s.best[1][w] > v ? s.best[1][w] : v;
   }
-  return v;
 }
 
 // Exclusive prefix over the workgroup, and the sum in `all`.
-__device__ __forceinline__ uint64_t block_prefix(Shared& s, uint64_t v, uint64_t& all) {
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const uint64_t inc = wave_prefix(v);
+template <class X>
+__device__ __forceinline__ X block_prefix(Shared& s, X v, X& all) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const X inc = wave_prefix(v);
   __syncthreads();
   if (lane == 63) s.part[wave] = inc;
   __syncthreads();
-  uint64_t before = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    const uint64_t q = s.part[w];
-    before += w < wave ? q : 0;
-    total += q;
-  }
-  all = total;
+  // each row of 16 lanes goes through the waves' sums
+  X sums = (X)s.part[lane & (kWaves - 1)];
+  sums += moved<kShift1>(sums);
+  sums += moved<kShift2>(sums);
+  sums += moved<kShift4>(sums);
+  sums += moved<kShift8>(sums);
+  all = last_lane(sums);
+  const X before = wave ? read_lane(sums, wave - 1) : 0;
   return before + inc - v;
 }
 
@@ -159,28 +183,48 @@ struct Row {
     // 2^52 on top leaves the number in the low bits, rounded to a whole one
     return __builtin_bit_cast(uint64_t, __builtin_bit_cast(double, bits) + 0x1p52) & 0xfffffffffffffull;
   }
-  // f(logit, id) for the ids of [a, b) by the lanes `lane` of n, and for a few
-  // that are not there, as logits that are no numbers. AHEAD loads at a time:
-  // as many as registers allow.
+  // f(logits, first id) for PER ids at a time of [a, b), by the lanes `lane` of n;
+  // ids from b on come as logits that are no numbers. AHEAD loads of a lane are on
+  // their way at any time, without a branch of its own in between.
   template <int AHEAD, class F>
   __device__ __forceinline__ void each(int a, int b, int lane, int n, F f) const {
-    for (int i = a + lane * PER; i < b; i += n * PER * AHEAD) {
-      Some w[AHEAD];
+    const int step = n * PER, full = (b - a) / step;
+    const T* at = x + a + lane * PER;
+    float v[PER];
+    Some w[AHEAD];
+    if (full > 0) {
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) w[k] = *(const Some*)(at + (int64_t)(k < full ? k : full - 1) * step);
+    }
+    for (int i = 0; i < full; i += AHEAD) {
 #pragma unroll
       for (int k = 0; k < AHEAD; ++k) {
-        const int at = i + k * n * PER;
-        if (at + PER <= b) {
-          w[k] = *(const Some*)(x + at);
-        } else {
+        if (i + k < full) {
 #pragma unroll
-          for (int e = 0; e < PER; ++e) w[k][e] = at + e < b ? x[at + e] : (T)__builtin_nanf("");
+          for (int e = 0; e < PER; ++e) v[e] = (float)w[k][e];
+          const int next = i + k + AHEAD;
+          w[k] = *(const Some*)(at + (int64_t)(next < full ? next : full - 1) * step);
+          f(v, a + (i + k) * step + lane * PER);
         }
       }
-#pragma unroll
-      for (int k = 0; k < AHEAD; ++k)
-#pragma unroll
-        for (int e = 0; e < PER; ++e) f((float)w[k][e], i + k * n * PER + e);
     }
+    const int first = a + full * step + lane * PER;
+    if (a + full * step < b) {
+#pragma unroll
+      for (int e = 0; e < PER; ++e) v[e] = first + e < b ? (float)x[first + e] : __builtin_nanf("");
+      f(v, first);
+    }
+  }
+  // the sum of the weights of what is wanted of [a, b), by the wave's lanes
+  template <class F>
+  __device__ __forceinline__ uint64_t sum(int a, int b, int lane, F wanted) const {
+    uint64_t all = 0;
+    each<2>(a, b, lane, 64, [&](const float (&v)[PER], int id) {
+#pragma unroll
+      for (int e = 0; e < PER; ++e)
+        if (wanted(v[e], id + e)) all += weight(v[e]);
+    });
+    return all;
   }
 };
 
@@ -191,8 +235,10 @@ struct FromRow {
   const Row<T>& row;
   template <class F>
   __device__ __forceinline__ void operator()(F f) const {
-    row.template each<1>(0, row.vocab, threadIdx.x, kLanes, [&](float v, int id) {
-      if (v >= row.least) f(place_of(key_of(v), id), v);
+    row.template each<1>(0, row.vocab, threadIdx.x, kLanes, [&](const float (&v)[Row<T>::PER], int id) {
+#pragma unroll
+      for (int e = 0; e < Row<T>::PER; ++e)
+        if (v[e] >= row.least) f(place_of(key_of(v[e]), id + e), v[e]);
     });
   }
 };
@@ -264,6 +310,13 @@ __device__ __forceinline__ uint64_t goal_of(float share, uint64_t sum) {
   return goal < 1 ? 1 : goal > sum ? sum : goal;
 }
 
+// the sum that a random number stands for: the token is the first to pass it
+__device__ __forceinline__ uint64_t chosen_of(float u, uint64_t all) {
+  const double at = (double)(u > 0.0f ? u : 0.0f) * (double)all;
+  const uint64_t goal = at < (double)all ? (uint64_t)at : all - 1;
+  return goal < all ? goal : all - 1;
+}
+
 template <class S>
 __device__ __forceinline__ uint64_t count_of(Shared& s, const S& source) {
   uint64_t n = 0, all;
@@ -279,34 +332,88 @@ __device__ __forceinline__ uint64_t mass_from(Shared& s, const Row<T>& row, cons
   return all;
 }
 
-// One workgroup a row. Three ways to the border:
+constexpr int kPairs = 256;                          // tokens that are compared each with each
+
+// What a row keeps of up to kPairs listed tokens, among them all that are larger
+// than one of them (or than `goal` allows, where that is given): each token's rank
+// and the sum of the larger ones' p, by comparing all with all (4 to 16 lanes a
+// token). goal 0: by top_p of the k largest; otherwise the sum that those kept
+// reach. For the lane that a token is with: its place, its weight and whether it
+// is kept; in the others `kept` is false. The last one kept goes to s.place.
+struct Token {
+  uint64_t place, weight;
+  bool kept;
+};
+template <class T>
+__device__ __forceinline__ Token compare_all(Shared& s, const Row<T>& row, int n, int k, float top_p, uint64_t goal) {
+  const int tid = threadIdx.x;
+  if (tid < n) s.mass[tid] = row.weight(of_key((uint32_t)(s.list[tid] >> 32)));
+  __syncthreads();
+  const int lanes = n <= 64 ? 16 : n <= 128 ? 8 : 4, mine = tid / lanes, at = mine < n ? mine : n - 1;
+  Token t{s.list[at], s.mass[at], mine < n && tid % lanes == 0};
+  uint32_t rank = 0;
+  uint64_t above = 0;
+  for (int j = tid % lanes; j < n; j += lanes) {
+    const bool larger = s.list[j] > t.place;
+    rank += larger;
+    above += larger ? s.mass[j] : 0;
+  }
+  rank = near_sum(rank, lanes);
+  above = near_sum(above, lanes);
+  if (k > 0) t.kept &= rank < (uint32_t)k;
+  if (goal || top_p < 1.0f) {
+    if (!goal) {
+      uint64_t sum;
+      block_prefix(s, t.kept ? t.weight : 0, sum);
+      goal = goal_of(top_p, sum);
+    }
+    t.kept &= above < goal;
+  }
+  if (t.kept && above < goal && above + t.weight >= goal) s.place = t.place;
+  return t;
+}
+
+// One workgroup a row. Ways to what is kept:
 //  * top_k up to kMostK: at least k tokens are as large as the k-th largest of the
-//    lanes' own largest logits, and hardly more; those are listed, and the rest
-//    of the work is on the list;
-//  * top_p: each wave sums the p of its stretch of the row by value, in bins of
-//    1/16 power of two; the tokens of the bin that the border falls into are
-//    listed;
-//  * anything else (larger k, more tokens than the list takes): searches over the row.
-// The token is then looked for in the stretch of the row, a sixteenth of it, that
-// the sums of the kept p point at.
+//    lanes' own largest logits, and hardly more; those are listed. With min_p
+//    those that it leaves are.
+//  * top_p without them, or more than the list takes: each wave sums the p of its
+//    stretch of the row by value, in bins of 1/16 power of two; the tokens of the
+//    bin that the border falls into are listed.
+//  * anything else: searches over the row.
+// Up to kPairs listed tokens are compared each with each, of more the border is
+// searched for with histograms. The token is then, if all that is kept was
+// compared, among them; otherwise it is looked for in the stretch of the row, a
+// sixteenth of it, that the sums of the kept p point at.
 template <class T>
 __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
   __shared__ Shared s;
-  const int r = blockIdx.x, tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int r = blockIdx.x, tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   Row<T> row;
   row.x = (const T*)p.x + r * p.stride;
   row.vocab = p.vocab;
   const float t = p.temperature ? p.temperature[r] : 1.0f, u = p.uniform[r];
   const int k = p.top_k ? p.top_k[r] : 0;
   const float top_p = p.top_p ? p.top_p[r] : 1.0f, min_p = p.min_p ? p.min_p[r] : 0.0f;
-  constexpr int PER = Row<T>::PER, W = 1;
+  constexpr int PER = Row<T>::PER;
   // a wave's stretch of the row, in whole steps of the wave
   const int stretch = (row.vocab + kWaves * 64 * PER - 1) / (kWaves * 64 * PER) * (64 * PER);
   const int from = wave * stretch < row.vocab ? wave * stretch : row.vocab, to = from + stretch < row.vocab ? from + stretch : row.vocab;
+  if (tid < kWaves) s.stretch[tid] = 0;
+  if (tid == 0) s.listed = 0;
+  s.count[tid] = 0;
 
   float most = -__builtin_inff();
-  row.template each<4>(from, to, lane, 64, [&](float v, int) { most = fmaxf(most, v); });
-  const uint32_t mine = key_of(most), top_key = block_max(s, mine);
+  row.template each<8>(from, to, lane, 64, [&](const float (&v)[PER], int) {
+#pragma unroll
+    for (int e = 0; e < PER; ++e) most = fmaxf(most, v[e]);
+  });
+  row.scale = 1.4426950408889634074 / (double)t;
+  const double log_p = min_p > 0.0f && min_p < 1.0f ? log2((double)min_p) : 0.0;
+  const uint32_t mine = key_of(most);
+  uint32_t top_key = mine, low_key = ~mine;            // of the lanes' largest the largest and the smallest
+  block_max(s, top_key, low_key);
+  low_key = ~low_key;
   if (top_key <= kNever) {
     if (tid == 0) {
       p.ids[r] = -1;
@@ -316,110 +423,100 @@ __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
   }
   row.top = of_key(top_key);
   if (!(t > 0.0f)) {
-    uint32_t first = 0;                                // the lowest id, as the largest of its complements
+    uint32_t first = 0, none = 0;                      // the lowest id, as the largest of its complements
     if (mine == top_key)
-      row.template each<4 / (PER / 4)>(from, to, lane, 64, [&](float v, int id) {
-        if (v == row.top && ~(uint32_t)id > first) first = ~(uint32_t)id;
+      row.template each<2>(from, to, lane, 64, [&](const float (&v)[PER], int id) {
+#pragma unroll
+        for (int e = 0; e < PER; ++e)
+          if (v[e] == row.top && ~(uint32_t)(id + e) > first) first = ~(uint32_t)(id + e);
       });
-    first = ~block_max(s, first);
+    block_max(s, first, none);
     if (tid == 0) {
-      p.ids[r] = (int32_t)first;
+      p.ids[r] = (int32_t)~first;
       if (p.logprob) p.logprob[r] = 0.0f;
     }
     return;
   }
   const bool infinite = !(row.top < __builtin_inff());
   row.base = (double)row.top;
-  row.scale = 1.4426950408889634074 / (double)t;
   row.floor = infinite ? 0.0 : -1000.0;
   row.least = infinite ? row.top : -0x1.fffffep127f;
-  if (min_p > 0.0f && !infinite) {
-    // the smallest logit of exponent log2(min_p) or more
-    const double least = min_p < 1.0f ? log2((double)min_p) : 0.0;
-    uint32_t key = kNever + 1, enough = top_key;
-    while (key < enough) {
-      const uint32_t mid = key + (enough - key) / 2;
-      if (((double)of_key(mid) - row.base) * row.scale >= least) enough = mid;
-      else key = mid + 1;
-    }
-    row.least = of_key(key);
-  }
-  const uint64_t lowest = place_of(key_of(row.least), ~0u), highest = place_of(top_key, 0);
-
-  uint64_t border = lowest;                            // tokens from it on, in order, are kept
-  bool summed = false;                                 // s.stretch holds the sums of what is kept
-  const FromRow<T> whole{row};
-  const auto search_row = [&] {
-    // on the row itself
-    if (k > 0 && count_of(s, whole) > (uint64_t)k) border = find_border<false>(s, row, whole, lowest, highest, k);
-    if (top_p < 1.0f)
-      border = find_border<true>(s, row, whole, border, highest, goal_of(top_p, mass_from(s, row, whole, border)));
-  };
-  // adds the kept tokens of the list to their stretches
-  const auto sum_list = [&](int n) {
-    for (int i = tid; i < n; i += kLanes) {
-      const uint64_t q = s.list[i];
-      if (q >= border) atomicAdd(&s.stretch[~(uint32_t)q / (uint32_t)stretch], (unsigned long long)row.weight(of_key((uint32_t)(q >> 32))));
-    }
-  };
-  if (tid < kWaves) s.stretch[tid] = 0;
-  if (tid == 0) s.listed = 0;
-  if (k > 0 && k <= kMostK) {
-    // a bound that at least k lanes' largest reach: the lower end of the bin of
-    // the k-th largest, of kLanes bins between the smallest and the largest of them
-    const uint32_t floor_key = key_of(row.least);
-    uint32_t bound = floor_key;
-    {
-      const uint32_t low = ~block_max(s, ~mine);
-      const float lo = fmaxf(of_key(low), -0x1.fffffep127f), by = (float)kLanes / (row.top - lo);
-      s.count[tid] = 0;
-      __syncthreads();
-      const auto bin_of = [&](float v) {
-        return (int)fminf(fmaxf((row.top - v) * by, 0.0f), kLanes - 1.0f);   // no number (0 by infinity): 0
-      };
-      const int b = bin_of(most);
-      if (mine >= floor_key) atomicAdd(&s.count[b], 1u);
-      __syncthreads();
-      uint64_t all;
-      const uint64_t c = s.count[tid], before = block_prefix(s, c, all);
-      if (before < (uint64_t)k && before + c >= (uint64_t)k) s.bin = tid;
-      if (all >= (uint64_t)k) {
-        // the smallest of the bin's own
-        __syncthreads();
-        const int last = s.bin;
-        bound = ~block_max(s, mine >= floor_key && b <= last ? ~mine : 0);
+  const bool some = min_p > 0.0f && !infinite;
+  if (some) {
+    // the smallest logit of exponent log2(min_p) or more: from where it should be
+    // outwards in growing steps, then halving
+    const auto enough = [&](uint32_t key) { return ((double)of_key(key) - row.base) * row.scale >= log_p; };
+    const double about = row.base + log_p / row.scale;
+    uint32_t yes = top_key, no = kNever;               // no logit at all is not enough
+    uint32_t key = about > -0x1.fffffep127 ? key_of((float)about) : kNever + 1;
+    key = key > top_key ? top_key : key;
+    for (uint32_t step = 1; yes - no > 1; step *= 8) {
+      if (enough(key)) {
+        yes = key;
+        if (no != kNever) break;
+        key = yes - no > step ? yes - step : no + 1;
+      } else {
+        no = key;
+        if (yes != top_key) break;
+        key = yes - no > step ? no + step : yes - 1;
       }
+      if (step >= 1u << 27) break;
     }
-    __syncthreads();
-    row.template each<4 / (PER / 4)>(from, to, lane, 64, [&](float v, int id) {
-      if (!(v >= row.least)) return;
-      const uint32_t key = key_of(v);
-      if (key < bound) return;
-      const int at = atomicAdd(&s.listed, 1);
-      if (at < kList) s.list[at] = place_of(key, id);
+    while (yes - no > 1) {
+      const uint32_t mid = no + (yes - no) / 2;
+      if (enough(mid)) yes = mid;
+      else no = mid;
+    }
+    row.least = of_key(yes);
+  }
+  // lists the tokens that are wanted; how many there are
+  const auto list = [&](auto wanted) {
+    row.template each<8>(from, to, lane, 64, [&](const float (&v)[PER], int id) {
+      uint32_t bits = 0;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) bits |= (uint32_t)(v[e] >= row.least && wanted(v[e])) << e;
+      if (!bits) return;
+      int at = atomicAdd(&s.listed, __popc(bits));
+#pragma unroll
+      for (int e = 0; e < PER; ++e)
+        if (bits >> e & 1) {
+          if (at < kList) s.list[at] = place_of(key_of(v[e]), id + e);
+          ++at;
+        }
     });
     __syncthreads();
-    const int n = s.listed;
-    if (n <= kList) {
-      const FromList listed{s, n};
-      const uint64_t bottom = place_of(bound, ~0u);
-      border = bottom;
-      if (n > k) border = find_border<false>(s, row, listed, bottom, highest, k);
-      if (top_p < 1.0f)
-        border = find_border<true>(s, row, listed, border, highest, goal_of(top_p, mass_from(s, row, listed, border)));
-      sum_list(n);
-      summed = true;
-    } else {
-      search_row();
+    return s.listed;
+  };
+  int n = kList + 1;                                   // listed tokens; too many for the list: none
+  uint64_t rest = 0;                                   // of those listed, the sum that the kept ones reach, where the larger ones are not listed
+  const bool by_count = k > 0 && k <= kMostK;
+  if (by_count || (some && k <= 0)) {
+    float by = 0.0f, past = __builtin_nanf("");        // no number: nothing is past the last bin wanted
+    if (by_count) {
+      // the bin of the k-th largest of the lanes' largest, of kLanes bins between
+      // the smallest and the largest of them; all where not so many lanes have any
+      by = (float)kLanes / (row.top - fmaxf(of_key(low_key), -0x1.fffffep127f));
+      if (most >= row.least) atomicAdd(&s.count[(int)fminf(fmaxf((row.top - most) * by, 0.0f), kLanes - 1.0f)], 1u);   // no number (0 by infinity): 0
+      if (tid == 0) s.bin = kLanes;
+      __syncthreads();
+      uint32_t all;
+      const uint32_t c = s.count[tid], before = block_prefix(s, c, all);
+      if (before < (uint32_t)k && before + c >= (uint32_t)k) s.bin = tid;
+      __syncthreads();
+      if (s.bin < kLanes - 1) past = s.bin + 1.0f;
     }
-  } else if (k <= 0 && top_p < 1.0f) {
+    n = list([&](float v) { return !((row.top - v) * by >= past); });
+  }
+  if (n > kList && k <= 0 && top_p < 1.0f) {
     const float by = fminf(kBinsPerPower * (float)row.scale, 1e30f);
-    const auto bin_of = [&](float v) {
-      return (int)fminf(fmaxf((row.top - v) * by, 0.0f), kMassBins - 1.0f);  // no number (of infinite logits): 0
-    };
+    const auto bin_of = [&](float v) { return (int)fminf(fmaxf((row.top - v) * by, 0.0f), kMassBins - 1.0f); };  // no number (of infinite logits): 0
+    __syncthreads();
+    if (tid == 0) s.listed = 0;
     for (int i = lane; i < kMassBins; i += 64) s.wave_mass[wave][i] = 0;
-    row.template each<W>(from, to, lane, 64, [&](float v, int) {
-      if (v >= row.least) atomicAdd(&s.wave_mass[wave][bin_of(v)], (unsigned long long)row.weight(v));
+    row.template each<2>(from, to, lane, 64, [&](const float (&v)[PER], int) {
+#pragma unroll
+      for (int e = 0; e < PER; ++e)
+        if (v[e] >= row.least) atomicAdd(&s.wave_mass[wave][bin_of(v[e])], (unsigned long long)row.weight(v[e]));
     });
     __syncthreads();
     uint64_t in_bin = 0, all;
@@ -433,42 +530,72 @@ __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
     }
     __syncthreads();
     const int last = s.bin;
-    const uint64_t rest = goal - s.above;
+    rest = goal - s.above;
     uint64_t larger = 0;
     for (int i = lane; i < last; i += 64) larger += s.wave_mass[wave][i];
     larger = wave_sum(larger);
-    row.template each<4 / (PER / 4)>(from, to, lane, 64, [&](float v, int id) {
-      if (!(v >= row.least) || bin_of(v) != last) return;
-      const int at = atomicAdd(&s.listed, 1);
-      if (at < kList) s.list[at] = place_of(key_of(v), id);
+    const float least_of = last, past = last < kMassBins - 1 ? last + 1.0f : __builtin_nanf("");
+    n = list([&](float v) {
+      const float y = (row.top - v) * by;
+      return !(y < least_of) && !(y >= past);
     });
-    __syncthreads();
-    const int n = s.listed;
-    if (n <= kList) {
-      if (lane == 0) s.stretch[wave] = larger;
-      uint32_t hi = 0, lo = 0;                         // the list's largest key, and its smallest's complement
-      for (int i = tid; i < n; i += kLanes) {
-        const uint32_t key = (uint32_t)(s.list[i] >> 32);
-        hi = key > hi ? key : hi;
-        lo = ~key > lo ? ~key : lo;
+    if (n <= kList && lane == 0) s.stretch[wave] = larger;
+  }
+
+  uint64_t border = place_of(key_of(row.least), ~0u);  // tokens from it on, in order, are kept
+  bool summed = false;                                 // s.stretch holds the sums of what is kept
+  if (n <= kPairs) {
+    const Token one = compare_all(s, row, n, rest ? 0 : k, rest ? 1.0f : top_p, rest);
+    if (!rest) {
+      // all that is kept is here: the token among them, by their ids
+      uint64_t all, before = 0;
+      block_prefix(s, one.kept ? one.weight : 0, all);
+      const int lanes = n <= 64 ? 16 : n <= 128 ? 8 : 4, e = tid / lanes;
+      if (!one.kept && e < n && tid % lanes == 0) s.mass[e] = 0;
+      __syncthreads();
+      const uint64_t goal = chosen_of(u, all);
+      const uint32_t id = ~(uint32_t)one.place;
+      for (int j = tid % lanes; j < n; j += lanes) before += ~(uint32_t)s.list[j] < id ? s.mass[j] : 0;
+      before = near_sum(before, lanes);
+      if (one.kept && before <= goal && goal < before + one.weight) {
+        p.ids[r] = (int32_t)id;
+        if (p.logprob) p.logprob[r] = (float)log((double)one.weight / (double)all);
       }
-      hi = block_max(s, hi);
-      lo = ~block_max(s, lo);
-      border = find_border<true>(s, row, FromList{s, n}, place_of(lo, ~0u), place_of(hi, 0), rest);
-      sum_list(n);
-      summed = true;
-    } else {
-      search_row();
+      return;
     }
+    if (one.kept) atomicAdd(&s.stretch[~(uint32_t)one.place / (uint32_t)stretch], (unsigned long long)one.weight);
+    __syncthreads();
+    border = s.place;
+    summed = true;
+  } else if (n <= kList) {
+    const FromList listed{s, n};
+    uint32_t hi_key = 0, lo_key = 0;
+    for (int i = tid; i < n; i += kLanes) {
+      const uint32_t key = (uint32_t)(s.list[i] >> 32);
+      hi_key = key > hi_key ? key : hi_key;
+      lo_key = ~key > lo_key ? ~key : lo_key;
+    }
+    block_max(s, hi_key, lo_key);
+    const uint64_t hi = place_of(hi_key, 0);
+    border = place_of(~lo_key, ~0u);
+    if (!rest && k > 0 && n > k) border = find_border<false>(s, row, listed, border, hi, k);
+    if (top_p < 1.0f)
+      border = find_border<true>(s, row, listed, border, hi, rest ? rest : goal_of(top_p, mass_from(s, row, listed, border)));
+    for (int i = tid; i < n; i += kLanes) {
+      const uint64_t q = s.list[i];
+      if (q >= border) atomicAdd(&s.stretch[~(uint32_t)q / (uint32_t)stretch], (unsigned long long)row.weight(of_key((uint32_t)(q >> 32))));
+    }
+    summed = true;
   } else if (k > 0 || top_p < 1.0f) {
-    search_row();
+    const FromRow<T> whole{row};
+    const uint64_t hi = place_of(top_key, 0);
+    if (k > 0 && count_of(s, whole) > (uint64_t)k) border = find_border<false>(s, row, whole, border, hi, k);
+    if (top_p < 1.0f) border = find_border<true>(s, row, whole, border, hi, goal_of(top_p, mass_from(s, row, whole, border)));
   }
 
   const auto kept = [&](float v, int id) { return v >= row.least && place_of(key_of(v), id) >= border; };
   if (!summed) {
-    uint64_t sum = 0;
-    row.template each<W>(from, to, lane, 64, [&](float v, int id) { sum += kept(v, id) ? row.weight(v) : 0; });
-    sum = wave_sum(sum);
+    const uint64_t sum = wave_sum(row.sum(from, to, lane, kept));
     if (lane == 0) s.stretch[wave] = sum;
   }
   __syncthreads();
@@ -476,9 +603,7 @@ __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
   uint64_t all = 0;
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) all += s.stretch[w];
-  const double at = (double)(u > 0.0f ? u : 0.0f) * (double)all;
-  uint64_t goal = at < (double)all ? (uint64_t)at : all - 1;
-  goal = goal < all ? goal : all - 1;
+  const uint64_t goal = chosen_of(u, all);
   uint64_t run = 0;
   int chosen = 0;
   while (run + s.stretch[chosen] <= goal) run += s.stretch[chosen++];
@@ -486,9 +611,7 @@ __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
   const int a = chosen * stretch, piece = (stretch / (64 * PER) + kWaves - 1) / kWaves * (64 * PER);
   const int end = a + stretch < row.vocab ? a + stretch : row.vocab;
   const int pa = a + wave * piece < end ? a + wave * piece : end, pb = pa + piece < end ? pa + piece : end;
-  uint64_t sum = 0;
-  row.template each<1>(pa, pb, lane, 64, [&](float v, int id) { sum += kept(v, id) ? row.weight(v) : 0; });
-  sum = wave_sum(sum);
+  const uint64_t sum = wave_sum(row.sum(pa, pb, lane, kept));
   if (lane == 0) s.part[wave] = sum;
   __syncthreads();
   for (int w = 0; w < wave; ++w) run += s.part[w];
@@ -502,7 +625,7 @@ __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
       w[e] = kept(v, id) ? row.weight(v) : 0;
       of_lane += w[e];
     }
-    const uint64_t inc = wave_prefix(of_lane), step = shfl64(inc, 63);
+    const uint64_t inc = wave_prefix(of_lane), step = last_lane(inc);
     if (goal < run + step) {
       uint64_t upto = run + inc - of_lane;
       if (goal >= upto && goal < run + inc) {
