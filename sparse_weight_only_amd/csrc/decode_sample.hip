@@ -151,9 +151,9 @@ __device__ __forceinline__ X block_prefix(Shared& s, X v, X& all) {
 }
 
 // A row and what its weights follow from.
-template <class T>
+template <class T, int PER_>
 struct Row {
-  static constexpr int PER = 16 / sizeof(T);         // logits of a lane and load
+  static constexpr int PER = PER_;                   // logits of a lane and load, at most a row's
   typedef T Some __attribute__((ext_vector_type(PER), aligned(sizeof(T))));   // rows of any vocabulary: element alignment only
   const T* x;
   int vocab;
@@ -183,61 +183,56 @@ struct Row {
     // 2^52 on top leaves the number in the low bits, rounded to a whole one
     return __builtin_bit_cast(uint64_t, __builtin_bit_cast(double, bits) + 0x1p52) & 0xfffffffffffffull;
   }
+  // The PER logits from `at` on of those before `end`. A load that would pass the
+  // end comes back to it, without a branch, which would wait for every load.
+  __device__ __forceinline__ Some load(int at, int end) const { return *(const Some*)(x + (end - PER < at ? end - PER : at)); }
   // f(logits, first id) for PER ids at a time of [a, b), by the lanes `lane` of n;
-  // ids from b on come as logits that are no numbers. AHEAD loads of a lane are on
-  // their way at any time, without a branch of its own in between.
+  // those that a load past the end brings once more, or that are none, as no numbers.
+  // AHEAD loads of a lane are on their way at any time. One body for all of them:
+  // a row of a workgroup's own is gone through a few times, each time by other
+  // code, which costs more to fetch than to execute where it is long.
   template <int AHEAD, class F>
   __device__ __forceinline__ void each(int a, int b, int lane, int n, F f) const {
-    const int step = n * PER, full = (b - a) / step;
-    const T* at = x + a + lane * PER;
-    float v[PER];
+    const int step = n * PER;
+    int at = a + lane * PER;
+    if (a >= b) return;
     Some w[AHEAD];
-    if (full > 0) {
 #pragma unroll
-      for (int k = 0; k < AHEAD; ++k) w[k] = *(const Some*)(at + (int64_t)(k < full ? k : full - 1) * step);
-    }
-    for (int i = 0; i < full; i += AHEAD) {
+    for (int k = 0; k < AHEAD; ++k) w[k] = load(at + k * step, b);
+    for (int i = a; i < b; i += AHEAD * step) {
+      float v[AHEAD][PER];
 #pragma unroll
       for (int k = 0; k < AHEAD; ++k) {
-        if (i + k < full) {
 #pragma unroll
-          for (int e = 0; e < PER; ++e) v[e] = (float)w[k][e];
-          const int next = i + k + AHEAD;
-          w[k] = *(const Some*)(at + (int64_t)(next < full ? next : full - 1) * step);
-          f(v, a + (i + k) * step + lane * PER);
-        }
+        for (int e = 0; e < PER; ++e) v[k][e] = (float)w[k][e];
+        w[k] = load(at + (k + AHEAD) * step, b);
       }
-    }
-    const int first = a + full * step + lane * PER;
-    if (a + full * step < b) {
+      if (i + AHEAD * step > b) {
 #pragma unroll
-      for (int e = 0; e < PER; ++e) v[e] = first + e < b ? (float)x[first + e] : __builtin_nanf("");
-      f(v, first);
-    }
-  }
-  // the sum of the weights of what is wanted of [a, b), by the wave's lanes
-  template <class F>
-  __device__ __forceinline__ uint64_t sum(int a, int b, int lane, F wanted) const {
-    uint64_t all = 0;
-    each<2>(a, b, lane, 64, [&](const float (&v)[PER], int id) {
+        for (int k = 0; k < AHEAD; ++k)
 #pragma unroll
-      for (int e = 0; e < PER; ++e)
-        if (wanted(v[e], id + e)) all += weight(v[e]);
-    });
-    return all;
+          for (int e = 0; e < PER; ++e) v[k][e] = b - PER + e >= at + k * step || at + k * step <= b - PER ? v[k][e] : __builtin_nanf("");
+      }
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        const int id = at + k * step;
+        f(v[k], id < b - PER ? id : b - PER);
+      }
+      at += AHEAD * step;
+    }
   }
 };
 
 // Where the tokens that a search goes through come from: the row itself, or
 // what has been listed of it. f(place, logit) for each.
-template <class T>
+template <class R>
 struct FromRow {
-  const Row<T>& row;
+  const R& row;
   template <class F>
   __device__ __forceinline__ void operator()(F f) const {
-    row.template each<1>(0, row.vocab, threadIdx.x, kLanes, [&](const float (&v)[Row<T>::PER], int id) {
+    row.template each<1>(0, row.vocab, threadIdx.x, kLanes, [&](const float (&v)[R::PER], int id) {
 #pragma unroll
-      for (int e = 0; e < Row<T>::PER; ++e)
+      for (int e = 0; e < R::PER; ++e)
         if (v[e] >= row.least) f(place_of(key_of(v[e]), id + e), v[e]);
     });
   }
@@ -257,9 +252,9 @@ struct FromList {
 // The border among a source's places in [lo, hi], of which there is one at least:
 // the last one in order such that those up to it, counted (MASS: weighed), reach
 // `goal`, which all together do. A histogram of kBins intervals at a time.
-template <bool MASS, class T, class S>
-__device__ uint64_t find_border(Shared& s, const Row<T>& row, const S& source, uint64_t lo, uint64_t hi, uint64_t goal) {
-  while (true) {
+template <bool MASS, class R, class S>
+__device__ uint64_t find_border(Shared& s, const R& row, const S& source, uint64_t lo, uint64_t hi, uint64_t goal) {
+  for (int round = 0; round < 6; ++round) {            // 64 bits, 11 a round
     const uint64_t span = hi - lo;
     const int bits = span ? 64 - __clzll((long long)span) : 0, shift = bits > 11 ? bits - 11 : 0;
     for (int i = threadIdx.x; i < kBins; i += kLanes) {
@@ -300,6 +295,7 @@ __device__ uint64_t find_border(Shared& s, const Row<T>& row, const S& source, u
       return s.place;
     }
   }
+  return hi;
 }
 
 // goal of a sum: the least whole number that is `share` of `sum` or more, 1 at least
@@ -324,8 +320,8 @@ __device__ __forceinline__ uint64_t count_of(Shared& s, const S& source) {
   block_prefix(s, n, all);
   return all;
 }
-template <class T, class S>
-__device__ __forceinline__ uint64_t mass_from(Shared& s, const Row<T>& row, const S& source, uint64_t border) {
+template <class R, class S>
+__device__ __forceinline__ uint64_t mass_from(Shared& s, const R& row, const S& source, uint64_t border) {
   uint64_t n = 0, all;
   source([&](uint64_t p, float v) { n += p >= border ? row.weight(v) : 0; });
   block_prefix(s, n, all);
@@ -344,8 +340,8 @@ struct Token {
   uint64_t place, weight;
   bool kept;
 };
-template <class T>
-__device__ __forceinline__ Token compare_all(Shared& s, const Row<T>& row, int n, int k, float top_p, uint64_t goal) {
+template <class R>
+__device__ __forceinline__ Token compare_all(Shared& s, const R& row, int n, int k, float top_p, uint64_t goal) {
   const int tid = threadIdx.x;
   if (tid < n) s.mass[tid] = row.weight(of_key((uint32_t)(s.list[tid] >> 32)));
   __syncthreads();
@@ -385,17 +381,17 @@ __device__ __forceinline__ Token compare_all(Shared& s, const Row<T>& row, int n
 // searched for with histograms. The token is then, if all that is kept was
 // compared, among them; otherwise it is looked for in the stretch of the row, a
 // sixteenth of it, that the sums of the kept p point at.
-template <class T>
+template <class T, int PER>
 __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
   __shared__ Shared s;
   const int r = blockIdx.x, tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-  Row<T> row;
+  Row<T, PER> row;
   row.x = (const T*)p.x + r * p.stride;
   row.vocab = p.vocab;
   const float t = p.temperature ? p.temperature[r] : 1.0f, u = p.uniform[r];
   const int k = p.top_k ? p.top_k[r] : 0;
   const float top_p = p.top_p ? p.top_p[r] : 1.0f, min_p = p.min_p ? p.min_p[r] : 0.0f;
-  constexpr int PER = Row<T>::PER;
+  constexpr int LIGHT = PER == 1 ? 4 : 32 / PER, HEAVY = PER == 1 ? 2 : 8 / PER;   // loads on their way
   // a wave's stretch of the row, in whole steps of the wave
   const int stretch = (row.vocab + kWaves * 64 * PER - 1) / (kWaves * 64 * PER) * (64 * PER);
   const int from = wave * stretch < row.vocab ? wave * stretch : row.vocab, to = from + stretch < row.vocab ? from + stretch : row.vocab;
@@ -404,7 +400,7 @@ __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
   s.count[tid] = 0;
 
   float most = -__builtin_inff();
-  row.template each<8>(from, to, lane, 64, [&](const float (&v)[PER], int) {
+  row.template each<LIGHT>(from, to, lane, 64, [&](const float (&v)[PER], int) {
 #pragma unroll
     for (int e = 0; e < PER; ++e) most = fmaxf(most, v[e]);
   });
@@ -425,7 +421,7 @@ __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
   if (!(t > 0.0f)) {
     uint32_t first = 0, none = 0;                      // the lowest id, as the largest of its complements
     if (mine == top_key)
-      row.template each<2>(from, to, lane, 64, [&](const float (&v)[PER], int id) {
+      row.template each<1>(from, to, lane, 64, [&](const float (&v)[PER], int id) {
 #pragma unroll
         for (int e = 0; e < PER; ++e)
           if (v[e] == row.top && ~(uint32_t)(id + e) > first) first = ~(uint32_t)(id + e);
@@ -471,18 +467,21 @@ __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
   }
   // lists the tokens that are wanted; how many there are
   const auto list = [&](auto wanted) {
-    row.template each<8>(from, to, lane, 64, [&](const float (&v)[PER], int id) {
+    row.template each<LIGHT>(from, to, lane, 64, [&](const float (&v)[PER], int id) {
       uint32_t bits = 0;
 #pragma unroll
       for (int e = 0; e < PER; ++e) bits |= (uint32_t)(v[e] >= row.least && wanted(v[e])) << e;
       if (!bits) return;
       int at = atomicAdd(&s.listed, __popc(bits));
+      while (bits) {
+        const int e = __ffs(bits) - 1;
+        bits &= bits - 1;
+        float one = v[0];
 #pragma unroll
-      for (int e = 0; e < PER; ++e)
-        if (bits >> e & 1) {
-          if (at < kList) s.list[at] = place_of(key_of(v[e]), id + e);
-          ++at;
-        }
+        for (int i = 1; i < PER; ++i) one = i == e ? v[i] : one;
+        if (at < kList) s.list[at] = place_of(key_of(one), id + e);
+        ++at;
+      }
     });
     __syncthreads();
     return s.listed;
@@ -513,7 +512,7 @@ __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
     __syncthreads();
     if (tid == 0) s.listed = 0;
     for (int i = lane; i < kMassBins; i += 64) s.wave_mass[wave][i] = 0;
-    row.template each<2>(from, to, lane, 64, [&](const float (&v)[PER], int) {
+    row.template each<HEAVY>(from, to, lane, 64, [&](const float (&v)[PER], int) {
 #pragma unroll
       for (int e = 0; e < PER; ++e)
         if (v[e] >= row.least) atomicAdd(&s.wave_mass[wave][bin_of(v[e])], (unsigned long long)row.weight(v[e]));
@@ -587,15 +586,31 @@ __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
     }
     summed = true;
   } else if (k > 0 || top_p < 1.0f) {
-    const FromRow<T> whole{row};
+    const FromRow<Row<T, PER>> whole{row};
     const uint64_t hi = place_of(top_key, 0);
     if (k > 0 && count_of(s, whole) > (uint64_t)k) border = find_border<false>(s, row, whole, border, hi, k);
     if (top_p < 1.0f) border = find_border<true>(s, row, whole, border, hi, goal_of(top_p, mass_from(s, row, whole, border)));
   }
 
-  const auto kept = [&](float v, int id) { return v >= row.least && place_of(key_of(v), id) >= border; };
+  // the weights of the kept ones of [a, b), 64 ids at a time: f(weight, first id)
+  const auto each_kept = [&](int a, int b, auto f) {
+    T next = a + lane < b ? row.x[a + lane] : (T)__builtin_nanf("");
+    for (int i = a; i < b; i += 64) {
+      const float v = (float)next;
+      const int id = i + lane, ahead = id + 64;
+      if (ahead < b) next = row.x[ahead];
+      const bool kept = id < b && v >= row.least && place_of(key_of(v), id) >= border;
+      if (f(kept ? row.weight(v) : 0, i)) return;
+    }
+  };
   if (!summed) {
-    const uint64_t sum = wave_sum(row.sum(from, to, lane, kept));
+    uint64_t sum = 0;
+    row.template each<HEAVY>(from, to, lane, 64, [&](const float (&v)[PER], int id) {
+#pragma unroll
+      for (int e = 0; e < PER; ++e)
+        if (v[e] >= row.least && place_of(key_of(v[e]), id + e) >= border) sum += row.weight(v[e]);
+    });
+    sum = wave_sum(sum);
     if (lane == 0) s.stretch[wave] = sum;
   }
   __syncthreads();
@@ -608,41 +623,31 @@ __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
   int chosen = 0;
   while (run + s.stretch[chosen] <= goal) run += s.stretch[chosen++];
   // and in it, again by waves and then step by step of the one
-  const int a = chosen * stretch, piece = (stretch / (64 * PER) + kWaves - 1) / kWaves * (64 * PER);
+  const int a = chosen * stretch, piece = stretch / kWaves;
   const int end = a + stretch < row.vocab ? a + stretch : row.vocab;
   const int pa = a + wave * piece < end ? a + wave * piece : end, pb = pa + piece < end ? pa + piece : end;
-  const uint64_t sum = wave_sum(row.sum(pa, pb, lane, kept));
+  uint64_t sum = 0;
+  each_kept(pa, pb, [&](uint64_t w, int) {
+    sum += w;
+    return false;
+  });
+  sum = wave_sum(sum);
   if (lane == 0) s.part[wave] = sum;
   __syncthreads();
   for (int w = 0; w < wave; ++w) run += s.part[w];
   if (goal < run || goal >= run + sum) return;
-  for (int i = pa; i < pb; i += 64 * PER) {
-    uint64_t w[PER], of_lane = 0;
-#pragma unroll
-    for (int e = 0; e < PER; ++e) {
-      const int id = i + lane * PER + e;
-      const float v = id < pb ? (float)row.x[id] : __builtin_nanf("");
-      w[e] = kept(v, id) ? row.weight(v) : 0;
-      of_lane += w[e];
+  each_kept(pa, pb, [&](uint64_t w, int first) {
+    const uint64_t upto = run + wave_prefix(w);
+    if (goal < upto && goal >= upto - w) {
+      p.ids[r] = first + lane;
+      if (p.logprob) p.logprob[r] = (float)log((double)w / (double)all);
     }
-    const uint64_t inc = wave_prefix(of_lane), step = last_lane(inc);
-    if (goal < run + step) {
-      uint64_t upto = run + inc - of_lane;
-      if (goal >= upto && goal < run + inc) {
-#pragma unroll
-        for (int e = 0; e < PER; ++e) {
-          if (goal >= upto && goal < upto + w[e]) {
-            p.ids[r] = i + lane * PER + e;
-            if (p.logprob) p.logprob[r] = (float)log((double)w[e] / (double)all);
-          }
-          upto += w[e];
-        }
-      }
-      return;
-    }
-    run += step;
-  }
+    run = last_lane(upto);
+    return goal < run;
+  });
 }
+
+typedef void (*SampleFn)(SampleParams);
 
 }  // namespace
 
@@ -671,8 +676,11 @@ extern "C" int sgemv_sample(const sgemv_sampling* g, void* hip_stream) {
   p.vocab = g->vocab;
   (void)hipGetLastError();
   const dim3 grid((uint32_t)g->rows), block(kLanes);
-  if (g->dtype == SGEMV_F32) hipLaunchKernelGGL(sample_kernel<float>, grid, block, 0, (hipStream_t)hip_stream, p);
-  else if (g->dtype == SGEMV_F16) hipLaunchKernelGGL(sample_kernel<_Float16>, grid, block, 0, (hipStream_t)hip_stream, p);
-  else hipLaunchKernelGGL(sample_kernel<__bf16>, grid, block, 0, (hipStream_t)hip_stream, p);
+  // rows of fewer logits than a load takes: one by one
+  const bool tiny = g->vocab < 8;
+  const SampleFn fn = g->dtype == SGEMV_F32   ? tiny ? sample_kernel<float, 1> : sample_kernel<float, 4>
+                      : g->dtype == SGEMV_F16 ? tiny ? sample_kernel<_Float16, 1> : sample_kernel<_Float16, 8>
+                                              : tiny ? sample_kernel<__bf16, 1> : sample_kernel<__bf16, 8>;
+  hipLaunchKernelGGL(fn, grid, block, 0, (hipStream_t)hip_stream, p);
   return hipGetLastError() == hipSuccess ? SGEMV_OK : SGEMV_EHIP;
 }
