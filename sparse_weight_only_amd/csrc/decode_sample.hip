@@ -249,55 +249,6 @@ struct FromList {
   }
 };
 
-// The border among a source's places in [lo, hi], of which there is one at least:
-// the last one in order such that those up to it, counted (MASS: weighed), reach
-// `goal`, which all together do. A histogram of kBins intervals at a time.
-template <bool MASS, class R, class S>
-__device__ uint64_t find_border(Shared& s, const R& row, const S& source, uint64_t lo, uint64_t hi, uint64_t goal) {
-  for (int round = 0; round < 6; ++round) {            // 64 bits, 11 a round
-    const uint64_t span = hi - lo;
-    const int bits = span ? 64 - __clzll((long long)span) : 0, shift = bits > 11 ? bits - 11 : 0;
-    for (int i = threadIdx.x; i < kBins; i += kLanes) {
-      if (MASS) s.mass[i] = 0;
-      s.count[i] = 0;
-    }
-    __syncthreads();
-    source([&](uint64_t p, float v) {
-      if (p < lo || p > hi) return;
-      const uint32_t bin = (uint32_t)((hi - p) >> shift);
-      if (MASS) atomicAdd(&s.mass[bin], (unsigned long long)row.weight(v));
-      atomicAdd(&s.count[bin], 1u);
-    });
-    __syncthreads();
-    const int i0 = threadIdx.x * 2;
-    const uint64_t a = MASS ? s.mass[i0] : s.count[i0], b = MASS ? s.mass[i0 + 1] : s.count[i0 + 1];
-    uint64_t all;
-    const uint64_t before = block_prefix(s, a + b, all);
-    if (before < goal && before + a + b >= goal) {
-      const int second = before + a < goal;
-      s.bin = i0 + second;
-      s.above = before + (second ? a : 0);
-      s.bin_count = s.count[i0 + second];
-    }
-    __syncthreads();
-    goal -= s.above;
-    const uint64_t from = hi - ((uint64_t)s.bin << shift), rest = ((uint64_t)1 << shift) - 1;
-    lo = from - lo > rest ? from - rest : lo;
-    hi = from;
-    const bool one = s.bin_count == 1;
-    __syncthreads();
-    if (lo == hi) return hi;
-    if (one) {
-      source([&](uint64_t p, float) {
-        if (p >= lo && p <= hi) s.place = p;
-      });
-      __syncthreads();
-      return s.place;
-    }
-  }
-  return hi;
-}
-
 // goal of a sum: the least whole number that is `share` of `sum` or more, 1 at least
 __device__ __forceinline__ uint64_t goal_of(float share, uint64_t sum) {
   const double want = (double)sum * (double)share;
@@ -330,43 +281,87 @@ __device__ __forceinline__ uint64_t mass_from(Shared& s, const R& row, const S& 
 
 constexpr int kPairs = 256;                          // tokens that are compared each with each
 
-// What a row keeps of up to kPairs listed tokens, among them all that are larger
-// than one of them (or than `goal` allows, where that is given): each token's rank
-// and the sum of the larger ones' p, by comparing all with all (4 to 16 lanes a
-// token). goal 0: by top_p of the k largest; otherwise the sum that those kept
-// reach. For the lane that a token is with: its place, its weight and whether it
-// is kept; in the others `kept` is false. The last one kept goes to s.place.
+// Up to kPairs places, each with all: for the lane that a token is with (one of 4
+// to 16 neighbours) its place and weight, its rank and the weight of those larger;
+// `there` is false in the others. Weights stay in s.mass.
 struct Token {
-  uint64_t place, weight;
-  bool kept;
+  uint64_t place, weight, above;
+  uint32_t rank;
+  bool there;
 };
+__device__ __forceinline__ int lanes_of(int n) { return n <= 64 ? 16 : n <= 128 ? 8 : 4; }
 template <class R>
-__device__ __forceinline__ Token compare_all(Shared& s, const R& row, int n, int k, float top_p, uint64_t goal) {
+__device__ __forceinline__ Token compare_all(Shared& s, const R& row, const uint64_t* places, int n) {
   const int tid = threadIdx.x;
-  if (tid < n) s.mass[tid] = row.weight(of_key((uint32_t)(s.list[tid] >> 32)));
+  if (tid < n) s.mass[tid] = row.weight(of_key((uint32_t)(places[tid] >> 32)));
   __syncthreads();
-  const int lanes = n <= 64 ? 16 : n <= 128 ? 8 : 4, mine = tid / lanes, at = mine < n ? mine : n - 1;
-  Token t{s.list[at], s.mass[at], mine < n && tid % lanes == 0};
-  uint32_t rank = 0;
-  uint64_t above = 0;
+  const int lanes = lanes_of(n), mine = tid / lanes, at = mine < n ? mine : n - 1;
+  Token t{places[at], s.mass[at], 0, 0, mine < n && tid % lanes == 0};
   for (int j = tid % lanes; j < n; j += lanes) {
-    const bool larger = s.list[j] > t.place;
-    rank += larger;
-    above += larger ? s.mass[j] : 0;
+    const bool larger = places[j] > t.place;
+    t.rank += larger;
+    t.above += larger ? s.mass[j] : 0;
   }
-  rank = near_sum(rank, lanes);
-  above = near_sum(above, lanes);
-  if (k > 0) t.kept &= rank < (uint32_t)k;
-  if (goal || top_p < 1.0f) {
-    if (!goal) {
-      uint64_t sum;
-      block_prefix(s, t.kept ? t.weight : 0, sum);
-      goal = goal_of(top_p, sum);
-    }
-    t.kept &= above < goal;
-  }
-  if (t.kept && above < goal && above + t.weight >= goal) s.place = t.place;
+  t.rank = near_sum(t.rank, lanes);
+  t.above = near_sum(t.above, lanes);
   return t;
+}
+
+// The border among a source's places in [lo, hi], of which there is one at least:
+// the last one in order such that those up to it, counted (MASS: weighed), reach
+// `goal`, which all together do. A histogram of kBins intervals, of the one with
+// the border again where it holds too many to compare.
+template <bool MASS, class R, class S>
+__device__ uint64_t find_border(Shared& s, const R& row, const S& source, uint64_t lo, uint64_t hi, uint64_t goal) {
+  for (int round = 0; round < 6; ++round) {            // 64 bits, 11 a round
+    const uint64_t span = hi - lo;
+    const int bits = span ? 64 - __clzll((long long)span) : 0, shift = bits > 11 ? bits - 11 : 0;
+    for (int i = threadIdx.x; i < kBins; i += kLanes) {
+      if (MASS) s.mass[i] = 0;
+      s.count[i] = 0;
+    }
+    __syncthreads();
+    source([&](uint64_t p, float v) {
+      if (p < lo || p > hi) return;
+      const uint32_t bin = (uint32_t)((hi - p) >> shift);
+      if (MASS) atomicAdd(&s.mass[bin], (unsigned long long)row.weight(v));
+      atomicAdd(&s.count[bin], 1u);
+    });
+    __syncthreads();
+    const int i0 = threadIdx.x * 2;
+    const uint64_t a = MASS ? s.mass[i0] : s.count[i0], b = MASS ? s.mass[i0 + 1] : s.count[i0 + 1];
+    uint64_t all;
+    const uint64_t before = block_prefix(s, a + b, all);
+    if (before < goal && before + a + b >= goal) {
+      const int second = before + a < goal;
+      s.bin = i0 + second;
+      s.above = before + (second ? a : 0);
+      s.bin_count = s.count[i0 + second];
+    }
+    __syncthreads();
+    goal -= s.above;
+    const uint64_t from = hi - ((uint64_t)s.bin << shift), rest = ((uint64_t)1 << shift) - 1;
+    lo = from - lo > rest ? from - rest : lo;
+    hi = from;
+    const int n = s.bin_count;
+    __syncthreads();
+    if (lo == hi) return hi;
+    if (n <= kPairs) {
+      uint64_t* near = (uint64_t*)s.count;
+      if (threadIdx.x == 0) s.bin = 0;
+      __syncthreads();
+      source([&](uint64_t p, float) {
+        if (p >= lo && p <= hi) near[atomicAdd(&s.bin, 1)] = p;
+      });
+      __syncthreads();
+      const Token t = compare_all(s, row, near, n);
+      const uint64_t above = MASS ? t.above : t.rank, weight = MASS ? t.weight : 1;
+      if (t.there && above < goal && above + weight >= goal) s.place = t.place;
+      __syncthreads();
+      return s.place;
+    }
+  }
+  return hi;
 }
 
 // One workgroup a row. Ways to what is kept:
@@ -391,7 +386,7 @@ __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
   const float t = p.temperature ? p.temperature[r] : 1.0f, u = p.uniform[r];
   const int k = p.top_k ? p.top_k[r] : 0;
   const float top_p = p.top_p ? p.top_p[r] : 1.0f, min_p = p.min_p ? p.min_p[r] : 0.0f;
-  constexpr int LIGHT = PER == 1 ? 4 : 32 / PER, HEAVY = PER == 1 ? 2 : 8 / PER;   // loads on their way
+  constexpr int LIGHT = 4, HEAVY = PER == 1 ? 2 : 8 / PER;   // loads on their way
   // a wave's stretch of the row, in whole steps of the wave
   const int stretch = (row.vocab + kWaves * 64 * PER - 1) / (kWaves * 64 * PER) * (64 * PER);
   const int from = wave * stretch < row.vocab ? wave * stretch : row.vocab, to = from + stretch < row.vocab ? from + stretch : row.vocab;
@@ -544,25 +539,33 @@ __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
   uint64_t border = place_of(key_of(row.least), ~0u);  // tokens from it on, in order, are kept
   bool summed = false;                                 // s.stretch holds the sums of what is kept
   if (n <= kPairs) {
-    const Token one = compare_all(s, row, n, rest ? 0 : k, rest ? 1.0f : top_p, rest);
+    const Token one = compare_all(s, row, s.list, n);
+    bool kept = one.there;
     if (!rest) {
       // all that is kept is here: the token among them, by their ids
       uint64_t all, before = 0;
-      block_prefix(s, one.kept ? one.weight : 0, all);
-      const int lanes = n <= 64 ? 16 : n <= 128 ? 8 : 4, e = tid / lanes;
-      if (!one.kept && e < n && tid % lanes == 0) s.mass[e] = 0;
+      if (k > 0) kept &= one.rank < (uint32_t)k;
+      block_prefix(s, kept ? one.weight : 0, all);
+      if (top_p < 1.0f) {
+        kept &= one.above < goal_of(top_p, all);
+        block_prefix(s, kept ? one.weight : 0, all);
+      }
+      const int lanes = lanes_of(n);
+      if (one.there && !kept) s.mass[tid / lanes] = 0;
       __syncthreads();
       const uint64_t goal = chosen_of(u, all);
       const uint32_t id = ~(uint32_t)one.place;
       for (int j = tid % lanes; j < n; j += lanes) before += ~(uint32_t)s.list[j] < id ? s.mass[j] : 0;
       before = near_sum(before, lanes);
-      if (one.kept && before <= goal && goal < before + one.weight) {
+      if (kept && before <= goal && goal < before + one.weight) {
         p.ids[r] = (int32_t)id;
         if (p.logprob) p.logprob[r] = (float)log((double)one.weight / (double)all);
       }
       return;
     }
-    if (one.kept) atomicAdd(&s.stretch[~(uint32_t)one.place / (uint32_t)stretch], (unsigned long long)one.weight);
+    kept &= one.above < rest;
+    if (kept && one.above + one.weight >= rest) s.place = one.place;
+    if (kept) atomicAdd(&s.stretch[~(uint32_t)one.place / (uint32_t)stretch], (unsigned long long)one.weight);
     __syncthreads();
     border = s.place;
     summed = true;
