@@ -68,8 +68,14 @@ int make_shape(const Cache* c, const sgemv_seqs* s, int32_t tokens, int32_t head
   // 20.5 us, 25.5 as a tile of 128). Up to 128 rows the same, a few tiles each
   // for itself, over short contexts, where the larger kernel's start and end
   // weigh more (96 rows over 300 slots: 9.7 against 15.2 us, over 6000: 61.6
-  // against 31.9; 48 rows: 11.9 against 13.6, and 39.5 against 27.8).
-  h.few = rows <= (int64_t)16 * s->count || (rows <= (int64_t)128 * s->count && ctx <= 1024);
+  // against 31.9; 48 rows: 11.9 against 13.6, and 39.5 against 27.8). In 8 bits
+  // the tiles read half as much and the larger kernel converts on top: up to 4096
+  // (4 x 108 rows, 8 heads, over 2000 slots: 19.4 against 30.9 us, over 4000: 31.9
+  // against 33.3; 1 x 128 rows over 4000: 16.9 against 26.5). Through a window in
+  // 16 bits up to 2048 (4 x 96 rows, a window of 1000: 16.1 against 24.3, of 2000:
+  // 25.8 against 25.5, of 3000: 35.3 against 27.7; 1 x 128, of 2000: 15.8, 22.5).
+  const int64_t near = c->exps ? 4096 : c->window > 0 ? 2048 : 1024;
+  h.few = rows <= (int64_t)16 * s->count || (rows <= (int64_t)128 * s->count && ctx <= near);
   h.waves = !h.few ? sgemv_dev::kManyWaves : h.dp == 256 ? sgemv_dev::kFewWaves<256> : sgemv_dev::kFewWaves<128>;
   h.halves = !h.few && h.dp < 256 && rows <= (int64_t)128 * s->count;
   h.tile_rows = h.few ? 16 : h.halves ? sgemv_dev::kManyRows<true> : sgemv_dev::kManyRows<false>;
