@@ -34,8 +34,8 @@ template <int DP> constexpr int kManyLds = kManyStages * 2 * kManyBlock<DP> * DP
 // lane, is read with the transposing LDS load: of its 16 lanes, lane 4 i + j
 // names key i's columns 4 j .., and lane c gets column c of the 4 keys.
 //
-// EIGHT: the cache holds codes of 8 bits. They come through registers, two to
-// three blocks ahead, are converted once for all waves and written to the same
+// EIGHT: the cache holds codes of 8 bits. They come through registers, a
+// block or two ahead, are converted once for all waves and written to the same
 // places of LDS (every wave converting what it reads would take as many vector
 // operations as its softmax). Each wave brings 8 keys of a block (4 of the
 // widest), which share their exponents; of the block's others it reads the
@@ -333,9 +333,12 @@ struct Many {
   static constexpr int WAVE_KEYS = 64 / ROW_LANES;       // keys of a block that a wave brings
   static constexpr int GROUPS = B / 8;                   // 8 keys in a row share their page and their exponents
   using Piece = std::conditional_t<DP == 64, dword2, dword4>;
+  // blocks that are on their way in registers: as many as those leave room for
+  static constexpr int DEEP = DP == 128 ? 2 : 1;
   struct Raw {
     Piece k, v;
     uint32_t e;                                          // exponents of group lane % GROUPS
+    int keys;                                            // how many of the wave's keys there are
   };
   struct Units { int k, v; };                            // what a stage holds K and V in units of
 
@@ -348,37 +351,57 @@ struct Many {
     const int in_page = (1 << p.seq.page_shift) - 1;
     return addr(eh + ((uint64_t)(uint32_t)page * p.exp_page + (uint64_t)(uint32_t)((at & in_page) >> p.exp_shift) * (uint32_t)p.heads));
   }
-  // starts the loads of the block at kb; `pages` from lookup8(kb)
+  // Starts the loads of the block at kb; `pages` from lookup8(kb). Keys behind the
+  // end lie in the last key's page, and those of a page that is not there are read
+  // from the first one: convert() leaves them out.
   __device__ __forceinline__ void fetch8(int kb, int pages, Raw& x) const {
     const int in_page = (1 << p.seq.page_shift) - 1;
-    const int first = wave * WAVE_KEYS, key = lane / ROW_LANES, d = lane % ROW_LANES * CP;
+    const int first = wave * WAVE_KEYS, key = lane / ROW_LANES, d = lane % ROW_LANES * CP, column = WHOLE || d < p.dim ? d : 0;
     const int pg = __builtin_amdgcn_readlane(pages, first / 8), at = (slot(kb) + first) & in_page;
-    const bool in = p.seq.page_ok(pg) && kb + first + key < t.key1 && (WHOLE || d < p.dim);
-    x.k = load<Piece>(or_nothing(in, addr(kh + element(pg, p.k_page, at, p.k_slot)) + (key * p.k_slot + d)));
-    x.v = load<Piece>(or_nothing(in, addr(vh + element(pg, p.v_page, at, p.v_slot)) + (key * p.v_slot + d)));
+    const bool ok = p.seq.page_ok(pg);
+    x.keys = ok ? t.key1 - kb - first : 0;
+    const int page = ok ? pg : 0;
+    x.k = load<Piece>(addr(kh + element(page, p.k_page, at, p.k_slot)) + (uint32_t)(key * p.k_slot + column));
+    x.v = load<Piece>(addr(vh + element(page, p.v_page, at, p.v_slot)) + (uint32_t)(key * p.v_slot + column));
     // a group that is not there, or that no row sees, has no exponents
     const int gk = kb + 8 * (lane % GROUPS), ga = slot(gk);
-    const bool ok = gk < t.key1 && p.seq.page_ok(pages) && (!WINDOW || ga < p.sinks || ga + 7 >= t.low);
-    x.e = load<uint16_t>(or_nothing(ok, exps_at(pages, ga)));
+    const bool there = gk < t.key1 && p.seq.page_ok(pages) && (!WINDOW || ga < p.sinks || ga + 7 >= t.low);
+    x.e = load<uint16_t>(or_nothing(there, exps_at(pages, ga)));
   }
   // converts a block that has come into a stage
-  __device__ __forceinline__ Units convert(const Raw& x, int stage) {
+  __device__ __forceinline__ Units convert(Raw& x, int stage) {
+    const int key = lane / ROW_LANES, d = lane % ROW_LANES * CP;
+    {
+      const int ek = x.e & 255u, ev = x.e >> 8;
+      const bool news = ek > k_top || ev > v_top || (ek > Eight<T>::kTinyKey && ek < k_least) || (ev > Eight<T>::kTiny && ev < v_least);
+      if (__any(news)) {
+#pragma unroll 1
+        for (int g = 0; g < GROUPS; ++g) {
+          const int e = __builtin_amdgcn_readlane(x.e, g), gk = e & 255, gv = e >> 8;
+          k_top = gk > k_top ? gk : k_top;
+          v_top = gv > v_top ? gv : v_top;
+          k_least = gk > Eight<T>::kTinyKey && gk < k_least ? gk : k_least;
+          v_least = gv > Eight<T>::kTiny && gv < v_least ? gv : v_least;
+        }
+      }
+    }
+    if (!WHOLE || x.keys < WAVE_KEYS) {
+      const bool in = key < x.keys && (WHOLE || d < p.dim);
 #pragma unroll
-    for (int g = 0; g < GROUPS; ++g) {
-      const int e = __builtin_amdgcn_readlane(x.e, g), ek = e & 255, ev = e >> 8;
-      k_top = ek > k_top ? ek : k_top;
-      v_top = ev > v_top ? ev : v_top;
-      k_least = ek > Eight<T>::kTinyKey && ek < k_least ? ek : k_least;
-      v_least = ev > Eight<T>::kTiny && ev < v_least ? ev : v_least;
+      for (int u = 0; u < CP / 4; ++u) {
+        x.k[u] = in ? x.k[u] : 0;
+        x.v[u] = in ? x.v[u] : 0;
+      }
     }
     const int mine = __builtin_amdgcn_readlane(x.e, wave * WAVE_KEYS / 8);
     const float by_k = below(mine & 255, k_top), by_v = below(mine >> 8, v_top);
-    const int key = wave * WAVE_KEYS + lane / ROW_LANES, piece = lane % ROW_LANES * (CP / 8);
-    const uint32_t ks = lds + stage * 4 * STAGE + key * DP * 2, vs = ks + STAGE * 2;
+    const int row = wave * WAVE_KEYS + key, piece = d / 8;
+    const uint32_t ks = lds + stage * 4 * STAGE + row * DP * 2, vs = ks + STAGE * 2;
+    const uint32_t k_at = fresh((piece ^ k_mix(row)) * 16), v_at = fresh((piece ^ v_mix(row)) * 16);   // of piece + u: u * 16 ^ k_at
 #pragma unroll
     for (int u = 0; u < CP / 8; ++u) {
-      lds_store(ks + ((piece + u) ^ k_mix(key)) * 16, eight<T>(x.k[2 * u], x.k[2 * u + 1], by_k));
-      lds_store(vs + ((piece + u) ^ v_mix(key)) * 16, eight<T>(x.v[2 * u], x.v[2 * u + 1], by_v));
+      lds_store(ks + (k_at ^ u * 16), eight<T>(x.k[2 * u], x.k[2 * u + 1], by_k));
+      lds_store(vs + (v_at ^ u * 16), eight<T>(x.v[2 * u], x.v[2 * u + 1], by_v));
     }
     return Units{k_top, v_top};
   }
@@ -415,6 +438,7 @@ struct Many {
         const int d = 16 * j + 8 * h;
         const dword2 w8 = load<dword2>(or_nothing(ok && (WHOLE || d < p.dim), addr(kr + d)));
         x = Half<T>::mma32(eight<T>(w8.x, w8.y, 1.0f), q[j], x);
+        if (j % 2) __builtin_amdgcn_sched_barrier(0);      // or all loads are issued first, into registers that are not there
       }
       const uint32_t bits = visible(kb) & there, own = bits >> (4 * h);
       float top = -__builtin_inff();
@@ -458,6 +482,7 @@ struct Many {
               o[i][4 * a + 1] += pk * __builtin_amdgcn_ldexpf(Half<T>::hi(lo), ev);
               o[i][4 * a + 2] += pk * __builtin_amdgcn_ldexpf(Half<T>::lo(hi), ev);
               o[i][4 * a + 3] += pk * __builtin_amdgcn_ldexpf(Half<T>::hi(hi), ev);
+              __builtin_amdgcn_sched_barrier(0);
             }
         }
       }
@@ -472,27 +497,28 @@ struct Many {
     k_least = v_least = 255;
 #pragma unroll
     for (int i = 0; i < OT; ++i) o[i] = f32x16{};
-    if (t.key0 >= t.key1) return;
+    if (t.key0 >= t.key1 || p.seq.n_pages == 0) return;
     const bool live = row0 < t.rows;
     const int blocks = (t.key1 - t.key0 + B - 1) / B;
     Raw even, odd;                                       // blocks on their way, by their numbers
     Units before = {0, 0}, now, next = {0, 0};           // of blocks i - 1, i, i + 1
     int pages;
     {
-      const int a = lookup8(t.key0), b = lookup8(t.key0 + B), d = lookup8(t.key0 + 2 * B);
+      const int a = lookup8(t.key0), b = lookup8(t.key0 + B), d = DEEP == 2 ? lookup8(t.key0 + 2 * B) : 0;
       fetch8(t.key0, a, even);
-      fetch8(t.key0 + B, b, odd);
-      pages = lookup8(t.key0 + 3 * B);
+      if (DEEP == 2) fetch8(t.key0 + B, b, odd);
+      pages = lookup8(t.key0 + (DEEP + 1) * B);
       now = convert(even, 0);
-      fetch8(t.key0 + 2 * B, d, even);
+      fetch8(t.key0 + DEEP * B, DEEP == 2 ? d : b, even);
     }
     const bool sound = pages_sound();
-    // block i + 1 into LDS, block i + 3 on its way, the pages of block i + 4
-    // (asked for first: loads return in order)
-    const auto ahead = [&](int i, Raw& r) {
-      const int later = lookup8(t.key0 + (i + 4) * B);
+    // block i + 1 into LDS, block i + 1 + DEEP on its way, the pages of the one
+    // after that (asked for first: loads return in order)
+    const auto ahead = [&](int i, Raw& r_) {
+      Raw& r = DEEP == 2 ? r_ : even;
+      const int later = lookup8(t.key0 + (i + 2 + DEEP) * B);
       next = convert(r, (i + 1) % ST);
-      fetch8(t.key0 + (i + 3) * B, pages, r);
+      fetch8(t.key0 + (i + 1 + DEEP) * B, pages, r);
       pages = later;
     };
     const auto begin = [&] { change_over<63>(); };

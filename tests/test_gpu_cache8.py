@@ -376,6 +376,61 @@ def test_attend8_exponents_far_apart(n, ctx, dim, dtype, far):
         assert (np.abs(got[i] - out[i]) <= tol).all(), (i, (np.abs(got[i] - out[i]) - tol).max())
 
 
+# room for more than 4096 slots a sequence, which the launch goes by: the kernel for many rows, in its form for few tokens
+ROOMY = [([60], [300], 16, 2, 1, 64, F16, 600), ([27, 33], [1100, 90], 16, 4, 2, 128, F16, 600), ([40], [40], 8, 3, 1, 128, BF16, 700),
+         ([25, 30], [2000, 1025], 8, 8, 2, 80, F16, 700), ([20], [1200], 16, 4, 1, 256, F16, 400), ([60, 1, 0], [200, 3000, 7], 128, 3, 3, 96, BF16, 60),
+         ([17], [17], 16, 1, 1, 16, F16, 600)]
+
+
+@pytest.mark.parametrize("case", ROOMY, ids=lambda c: f"n{len(c[0])}x{max(c[0])}_d{c[5]}")
+@pytest.mark.parametrize("block", [8, 16])
+def test_attend8_tiles_of_128_rows(case, block):
+    n, ctx, page, heads, kv, dim, dtype, per = case
+    say("case attend8 tiles of 128", case, block)
+    s = Setup8(n, ctx, page, heads, kv, dim, dtype, 13, per_seq=per, block=block, spread=6)
+    assert s.cache.plan(s.seqs, s.tokens, heads).tile_rows == (128 if dim <= 128 else 256)
+    s.check(s.cache.attend(s.seqs, s.q), s.want(), str(case))
+    bits = np.zeros((s.tokens, 3), np.uint32)
+    rng = np.random.default_rng(14)
+    for q in range(len(n)):
+        for i in range(n[q]):
+            for j in [i] + np.flatnonzero(rng.random(n[q]) < 0.4).tolist():
+                bits[s.new_start[q] + i, j // 32] |= np.uint32(1) << np.uint32(j % 32)
+    s.check(s.cache.attend(s.seqs, s.q, tree=ints(bits.view(np.int32))), s.want(tree=bits), str(case) + " tree")
+    # NaN where nobody looks, and exponents too far apart for one unit
+    s.k8.view(torch.uint8)[torch.from_numpy(s.unused).cuda()] = 0x7F
+    s.scales.view(torch.uint8)[s.pages[0, 0], 0, :, 1] = 60
+    s.values()
+    s.kc, s.vc = s.kc.nan_to_num(), s.vc.nan_to_num()
+    s.check(s.cache.attend(s.seqs, s.q), s.want(), str(case) + " far exponents")
+
+
+@pytest.mark.parametrize("kind,ctx,window", [(Setup, [2600, 150], 2100), (Setup8, [5000, 150], 4200)])
+@pytest.mark.parametrize("tree", [False, True])
+def test_window_tiles_of_128_rows(kind, ctx, window, tree):
+    say("case window tiles of 128", kind.__name__, ctx, window, tree)
+    s = kind([30, 20], ctx, 16, 2, 1, 64, F16, 15, per_seq=400)
+    assert s.cache.plan(s.seqs, s.tokens, 2, window=window, sinks=5).tile_rows == 128
+    bits = np.uint32(1) << (np.arange(50) % 30 % 20).astype(np.uint32) if tree else None
+    bits = None if bits is None else (bits | np.uint32(3))[:, None]
+    got = s.cache.attend(s.seqs, s.q, tree=None if bits is None else ints(bits.view(np.int32)), window=window, sinks=5)
+    want = odec.attend(host(s.q), host(s.kc), host(s.vc), s.new_start, s.ctx, s.pages, 0.125, bits, window, 5)
+    s.check(got, want, f"{ctx} {window}")
+
+
+def test_attend8_cache_without_pages():
+    say("case attend8 no pages")
+    empty = torch.zeros(0, 16, 1, 64, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    cache = sg.PagedCache8.from_tensors(empty, empty, torch.zeros(0, 2, 1, 2, dtype=torch.uint8, device="cuda").view(torch.float8_e8m0fnu))
+    for n in (1, 200):
+        seqs = sg.Sequences(ints([0, n]), ints([n + 5]), torch.zeros(1, 20, dtype=torch.int32, device="cuda"))
+        q = torch.randn(n, 2, 64, device="cuda").half()
+        for kw in ({}, dict(window=3, sinks=1)):
+            out = torch.full_like(q, 9.0)
+            assert not cache.attend(seqs, q, out=out, **kw).any()
+        assert cache.append(seqs, q[:, :1], q[:, :1], rope=sg.Rope(64), q=q).shape == q.shape
+
+
 def test_attend8_lengths_that_do_not_fit():
     say("case attend8 lengths")
     s = Setup8([3, 40], [50, 60], 16, 2, 1, 64, F16, 12, per_seq=4, spare=12)
