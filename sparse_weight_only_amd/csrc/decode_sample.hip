@@ -162,6 +162,13 @@ struct Row {
   double base, scale;                                // M and log2(e) / T
   double floor;                                      // of exponents: where M is infinite the others' do not count, and its own are 0
 
+  // y f + c. Left to itself the compiler moves every coefficient into the
+  // registers of the sum first, which is a third of the polynomial's time.
+  static __device__ __forceinline__ double step(double y, double f, double c) {
+    double r;
+    asm("v_fma_f64 %0, %1, %2, %3" : "=v"(r) : "v"(y), "v"(f), "s"(c));
+    return r;
+  }
   // 2^((x - M) scale) in units of 2^-43, rounded; for x from `least` on.
   __device__ __forceinline__ uint64_t weight(float v) const {
     // no number (infinities less each other) becomes the floor
@@ -169,15 +176,15 @@ struct Row {
     // the nearest whole number, in the low bits too
     const double big = z + 0x1.8p52, n = big - 0x1.8p52, f = z - n;
     double y = 0x1.b69b333333333p+19;                // 2^43 2^f
-    y = fma(y, f, 0x1.63f1a66666666p+23);
-    y = fma(y, f, 0x1.ffcb2e3333335p+26);
-    y = fma(y, f, 0x1.43088c34ccccbp+30);
-    y = fma(y, f, 0x1.5d87fea9ba666p+33);
-    y = fma(y, f, 0x1.3b2ab72c33333p+36);
-    y = fma(y, f, 0x1.c6b08d70374acp+38);
-    y = fma(y, f, 0x1.ebfbdff813d86p+40);
-    y = fma(y, f, 0x1.62e42fefa3a31p+42);
-    y = fma(y, f, 0x1.000000000003fp+43);
+    y = step(y, f, 0x1.63f1a66666666p+23);
+    y = step(y, f, 0x1.ffcb2e3333335p+26);
+    y = step(y, f, 0x1.43088c34ccccbp+30);
+    y = step(y, f, 0x1.5d87fea9ba666p+33);
+    y = step(y, f, 0x1.3b2ab72c33333p+36);
+    y = step(y, f, 0x1.c6b08d70374acp+38);
+    y = step(y, f, 0x1.ebfbdff813d86p+40);
+    y = step(y, f, 0x1.62e42fefa3a31p+42);
+    y = step(y, f, 0x1.000000000003fp+43);
     // times 2^n (n >= -1000: no subnormals)
     const uint64_t bits = __builtin_bit_cast(uint64_t, y) + ((uint64_t)__builtin_bit_cast(uint64_t, big) << 52);
     // 2^52 on top leaves the number in the low bits, rounded to a whole one
@@ -509,8 +516,12 @@ __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
     for (int i = lane; i < kMassBins; i += 64) s.wave_mass[wave][i] = 0;
     row.template each<HEAVY>(from, to, lane, 64, [&](const float (&v)[PER], int) {
 #pragma unroll
-      for (int e = 0; e < PER; ++e)
-        if (v[e] >= row.least) atomicAdd(&s.wave_mass[wave][bin_of(v[e])], (unsigned long long)row.weight(v[e]));
+      for (int e = 0; e < PER; ++e) {
+        // without branches, so that one weight's latencies are the others' time
+        uint64_t w = row.weight(v[e]);
+        asm("" : "+v"(w));
+        atomicAdd(&s.wave_mass[wave][bin_of(v[e])], (unsigned long long)(v[e] >= row.least ? w : 0));
+      }
     });
     __syncthreads();
     uint64_t in_bin = 0, all;
