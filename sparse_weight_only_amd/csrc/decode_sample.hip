@@ -14,6 +14,8 @@
 // polynomial of degree 9 on half a power of two to each side, within 2^-45),
 // and p is rounded to whole multiples of 2^-43, whose sums are exact and do not
 // depend on their order.
+#include <type_traits>
+
 #include "decode_internal.hpp"
 #include "launch_util.hpp"
 
@@ -26,6 +28,8 @@ constexpr int kUnit = 43;                            // p in units of 2^-43: 2^2
 constexpr int kMostVocab = 1 << 20;
 constexpr int kBins = 2048;                          // of a step of a search
 constexpr int kMassBins = 512, kBinsPerPower = 16;   // of a wave's masses by value: 16 to a power of two
+constexpr int kHeld = 32;                            // logits that a lane may hold
+typedef float floats __attribute__((ext_vector_type(kHeld)));
 constexpr int kList = 8192;                          // tokens that are looked at one by one
 constexpr int kMostK = 768;                          // see candidates()
 
@@ -383,7 +387,10 @@ __device__ uint64_t find_border(Shared& s, const R& row, const S& source, uint64
 // searched for with histograms. The token is then, if all that is kept was
 // compared, among them; otherwise it is looked for in the stretch of the row, a
 // sixteenth of it, that the sums of the kept p point at.
-template <class T, int PER>
+//
+// HELD, for rows that fit: what a lane reads of its wave's stretch stays in its
+// registers, and the row is read once.
+template <class T, int PER, bool HELD>
 __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
   __shared__ Shared s;
   const int r = blockIdx.x, tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
@@ -402,10 +409,45 @@ __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
   s.count[tid] = 0;
 
   float most = -__builtin_inff();
-  row.template each<LIGHT>(from, to, lane, 64, [&](const float (&v)[PER], int) {
+  floats held = {};
+  constexpr int LOADS = kHeld / PER;
+  if constexpr (HELD) {
+    typename Row<T, PER>::Some w[LOADS];
 #pragma unroll
-    for (int e = 0; e < PER; ++e) most = fmaxf(most, v[e]);
-  });
+    for (int k = 0; k < LOADS; ++k) w[k] = row.load(from + (k * 64 + lane) * PER, to);
+#pragma unroll
+    for (int k = 0; k < LOADS; ++k) {
+      const int at = from + (k * 64 + lane) * PER;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) {
+        const float v = at <= to - PER || to - PER + e >= at ? (float)w[k][e] : __builtin_nanf("");
+        held[k * PER + e] = v;
+        most = fmaxf(most, v);
+      }
+    }
+  } else {
+    row.template each<LIGHT>(from, to, lane, 64, [&](const float (&v)[PER], int) {
+#pragma unroll
+      for (int e = 0; e < PER; ++e) most = fmaxf(most, v[e]);
+    });
+  }
+  // f(logits, first id) for what the lane has of the wave's stretch
+  const auto own = [&](auto ahead, auto f) {
+    if constexpr (HELD) {
+#pragma unroll 1
+      for (int k = 0; k < LOADS; ++k) {
+        const int at = from + (k * 64 + lane) * PER;
+        float v[PER];
+#pragma unroll
+        for (int e = 0; e < PER; ++e) v[e] = held[k * PER + e];
+        f(v, at < to - PER ? at : to - PER);
+      }
+    } else {
+      row.template each<decltype(ahead)::value>(from, to, lane, 64, f);
+    }
+  };
+  const std::integral_constant<int, LIGHT> light{};
+  const std::integral_constant<int, HEAVY> heavy{};
   row.scale = 1.4426950408889634074 / (double)t;
   const double log_p = min_p > 0.0f && min_p < 1.0f ? log2((double)min_p) : 0.0;
   const uint32_t mine = key_of(most);
@@ -423,7 +465,7 @@ __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
   if (!(t > 0.0f)) {
     uint32_t first = 0, none = 0;                      // the lowest id, as the largest of its complements
     if (mine == top_key)
-      row.template each<1>(from, to, lane, 64, [&](const float (&v)[PER], int id) {
+      own(std::integral_constant<int, 1>{}, [&](const float (&v)[PER], int id) {
 #pragma unroll
         for (int e = 0; e < PER; ++e)
           if (v[e] == row.top && ~(uint32_t)(id + e) > first) first = ~(uint32_t)(id + e);
@@ -467,12 +509,17 @@ __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
     }
     row.least = of_key(yes);
   }
-  // lists the tokens that are wanted; how many there are
-  const auto list = [&](auto wanted) {
-    row.template each<LIGHT>(from, to, lane, 64, [&](const float (&v)[PER], int id) {
+  // lists the tokens from `bound` on that are wanted; how many there are
+  const auto list = [&](float bound, auto wanted) {
+    own(light, [&](const float (&v)[PER], int id) {
+      // most lanes have none: one look at the largest
+      float top = v[0];
+#pragma unroll
+      for (int e = 1; e < PER; ++e) top = fmaxf(top, v[e]);
+      if (!(top >= bound)) return;
       uint32_t bits = 0;
 #pragma unroll
-      for (int e = 0; e < PER; ++e) bits |= (uint32_t)(v[e] >= row.least && wanted(v[e])) << e;
+      for (int e = 0; e < PER; ++e) bits |= (uint32_t)(v[e] >= bound && wanted(v[e])) << e;
       if (!bits) return;
       int at = atomicAdd(&s.listed, __popc(bits));
       while (bits) {
@@ -492,11 +539,11 @@ __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
   uint64_t rest = 0;                                   // of those listed, the sum that the kept ones reach, where the larger ones are not listed
   const bool by_count = k > 0 && k <= kMostK;
   if (by_count || (some && k <= 0)) {
-    float by = 0.0f, past = __builtin_nanf("");        // no number: nothing is past the last bin wanted
+    float bound = row.least;
     if (by_count) {
       // the bin of the k-th largest of the lanes' largest, of kLanes bins between
       // the smallest and the largest of them; all where not so many lanes have any
-      by = (float)kLanes / (row.top - fmaxf(of_key(low_key), -0x1.fffffep127f));
+      const float by = (float)kLanes / (row.top - fmaxf(of_key(low_key), -0x1.fffffep127f));
       if (most >= row.least) atomicAdd(&s.count[(int)fminf(fmaxf((row.top - most) * by, 0.0f), kLanes - 1.0f)], 1u);   // no number (0 by infinity): 0
       if (tid == 0) s.bin = kLanes;
       __syncthreads();
@@ -504,9 +551,12 @@ __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
       const uint32_t c = s.count[tid], before = block_prefix(s, c, all);
       if (before < (uint32_t)k && before + c >= (uint32_t)k) s.bin = tid;
       __syncthreads();
-      if (s.bin < kLanes - 1) past = s.bin + 1.0f;
+      // its lower end, less what the roundings there and here may come to
+      const float end = row.top - (s.bin + 1.0f) / by;
+      const float lower = end - (__builtin_fabsf(row.top) + __builtin_fabsf(end)) * 0x1p-20f;
+      if (s.bin < kLanes - 1 && lower > bound) bound = lower;
     }
-    n = list([&](float v) { return !((row.top - v) * by >= past); });
+    n = list(bound, [](float) { return true; });
   }
   if (n > kList && k <= 0 && top_p < 1.0f) {
     const float by = fminf(kBinsPerPower * (float)row.scale, 1e30f);
@@ -514,7 +564,7 @@ __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
     __syncthreads();
     if (tid == 0) s.listed = 0;
     for (int i = lane; i < kMassBins; i += 64) s.wave_mass[wave][i] = 0;
-    row.template each<HEAVY>(from, to, lane, 64, [&](const float (&v)[PER], int) {
+    own(heavy, [&](const float (&v)[PER], int) {
 #pragma unroll
       for (int e = 0; e < PER; ++e) {
         // without branches, so that one weight's latencies are the others' time
@@ -540,7 +590,7 @@ __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
     for (int i = lane; i < last; i += 64) larger += s.wave_mass[wave][i];
     larger = wave_sum(larger);
     const float least_of = last, past = last < kMassBins - 1 ? last + 1.0f : __builtin_nanf("");
-    n = list([&](float v) {
+    n = list(row.least, [&](float v) {
       const float y = (row.top - v) * by;
       return !(y < least_of) && !(y >= past);
     });
@@ -619,7 +669,7 @@ __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
   };
   if (!summed) {
     uint64_t sum = 0;
-    row.template each<HEAVY>(from, to, lane, 64, [&](const float (&v)[PER], int id) {
+    own(heavy, [&](const float (&v)[PER], int id) {
 #pragma unroll
       for (int e = 0; e < PER; ++e)
         if (v[e] >= row.least && place_of(key_of(v[e]), id + e) >= border) sum += row.weight(v[e]);
@@ -662,6 +712,12 @@ __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
 }
 
 typedef void (*SampleFn)(SampleParams);
+template <class T>
+SampleFn pick(int vocab) {
+  constexpr int PER = 16 / sizeof(T);
+  // lanes hold what 16 of their waves' stretches, in whole steps, come to
+  return vocab < PER ? sample_kernel<T, 1, false> : vocab <= kLanes * kHeld ? sample_kernel<T, PER, true> : sample_kernel<T, PER, false>;
+}
 
 }  // namespace
 
@@ -691,10 +747,7 @@ extern "C" int sgemv_sample(const sgemv_sampling* g, void* hip_stream) {
   (void)hipGetLastError();
   const dim3 grid((uint32_t)g->rows), block(kLanes);
   // rows of fewer logits than a load takes: one by one
-  const bool tiny = g->vocab < 8;
-  const SampleFn fn = g->dtype == SGEMV_F32   ? tiny ? sample_kernel<float, 1> : sample_kernel<float, 4>
-                      : g->dtype == SGEMV_F16 ? tiny ? sample_kernel<_Float16, 1> : sample_kernel<_Float16, 8>
-                                              : tiny ? sample_kernel<__bf16, 1> : sample_kernel<__bf16, 8>;
+  const SampleFn fn = g->dtype == SGEMV_F32 ? pick<float>(g->vocab) : g->dtype == SGEMV_F16 ? pick<_Float16>(g->vocab) : pick<__bf16>(g->vocab);
   hipLaunchKernelGGL(fn, grid, block, 0, (hipStream_t)hip_stream, p);
   return hipGetLastError() == hipSuccess ? SGEMV_OK : SGEMV_EHIP;
 }

@@ -458,3 +458,127 @@ def test_streams_and_workspace():
     assert all(torch.equal(x, wa) and torch.equal(y, wb) for x, y in got)
     with pytest.raises(sg.SgemvError):
         a.cache.attend(a.seqs, a.q, workspace=room[:-8])
+
+
+def test_append8_lengths_that_do_not_fit():
+    """A sequence longer than its row of the page table ends with that row; one below 0 has no slots."""
+    say("case append8 lengths")
+    a, b = (Setup8([5, 3], [64, 3], 16, 2, 2, 32, F16, 21, per_seq=4, spare=6, block=16) for _ in range(2))
+    b.seqs.ctx_len.copy_(ints([10 ** 9, 3]))
+    for s in (a, b):
+        s.cache.append(s.seqs, s.k, s.v)
+    assert all(np.array_equal(x, y) for x, y in zip(state(a), state(b)))
+    before = state(a)
+    a.seqs.ctx_len.copy_(ints([0, -9]))
+    out = a.cache.append(a.seqs, a.k, a.v, rope=sg.Rope(32), q=a.q)
+    assert all(np.array_equal(x, y) for x, y in zip(state(a), before)) and torch.isfinite(out).all()
+
+
+# ------------------------------------------------------------ use together
+
+def ragged(lists, dtype):
+    start = np.concatenate([[0], np.cumsum([len(x) for x in lists])])
+    return torch.tensor([v for x in lists for v in x], dtype=dtype, device="cuda"), ints(start)
+
+
+def test_decode_step_in_8_bits():
+    """A prompt and five steps of two beams: the append, the attention through a
+    window, penalties and masks on logits, the choice of a token; every step
+    against FP64 on its own inputs."""
+    say("case decode step in 8 bits")
+    heads, kv, dim, vocab, page, block = 4, 2, 64, 3000, 16, 8
+    cache, rope = sg.PagedCache8(12, page, kv, dim, scale_slots=block), sg.Rope(dim)
+    turns = odec.rope_turns(dim)
+    window, sinks = 24, 3
+    g = torch.Generator(device="cuda").manual_seed(3)
+    prompt = torch.randn(40, kv, dim, device="cuda", generator=g).half()
+    pages = np.array([[3, 1, 7, 4], [3, 1, 5, 6]])             # the beams share the prompt's whole pages
+    cache.append(sg.Sequences(ints([0, 40]), ints([40]), ints(pages[:1])), prompt, prompt * 0.5, rope=rope)
+    for t in (cache.k, cache.v, cache.scales):                 # and have copies of the one that goes on
+        t.view(torch.uint8)[5] = t.view(torch.uint8)[7]
+    seqs = sg.Sequences(ints([0, 1, 2]), ints([40, 40]), ints(pages))
+    head = (0.3 * torch.randn(heads * dim, vocab, device="cuda", generator=g)).half()
+    rng = np.random.default_rng(4)
+    history, rep = [[1, 2], [2, 2]], torch.full((2,), 1.3, device="cuda")
+    allowed = torch.from_numpy(rng.random((2, vocab)) < 0.05).cuda()
+    words = torch.zeros(2, -(-vocab // 32) * 32, dtype=torch.int64, device="cuda")
+    words[:, :vocab] = allowed
+    words = (words.view(2, -1, 32) << torch.arange(32, device="cuda")).sum(-1)
+    masks = words.where(words < 1 << 31, words - (1 << 32)).int()
+    for step in range(5):
+        seqs.ctx_len += 1
+        q, k, v = (torch.randn(2, n, dim, device="cuda", generator=g).half() for n in (heads, kv, kv))
+        before = [t.contiguous().view(torch.uint8).cpu().numpy() for t in (cache.k, cache.v, cache.scales)]
+        q0 = host(q)
+        cache.append(seqs, k, v, rope=rope, q=q, q_out=q)
+        pos = [40 + step] * 2
+        assert (np.abs(host(q) - odec.rope(q0, pos, turns)) <= 2.0 ** -19 * np.abs(q0).max() + U[F16] * np.abs(host(q)) + A[F16]).all()
+        kk, vv, ss = (t.contiguous().view(torch.uint8).cpu().numpy() for t in (cache.k, cache.v, cache.scales))
+        v_ref, s_ref = odec.append8(before[1], before[2], host(v), 1, [0, 1, 2], [41 + step] * 2, pages)
+        assert np.array_equal(vv, v_ref) and np.array_equal(ss[..., 1], s_ref[..., 1])
+        out = cache.attend(seqs, q, window=window, sinks=sinks)
+        kd, vd = odec.values8(kk, ss, 0), odec.values8(vv, ss, 1)
+        ref, mean, worst, keys = odec.attend(host(q), kd, vd, [0, 1, 2], [41 + step] * 2, pages, dim ** -0.5, None, window, sinks)
+        tol = mean * (3 * U[F16] + 2 * dim * E * worst[:, :, None] + 2 * keys[:, :, None] * E) + keys[:, :, None] * A[F16] * 8 + A[F16]
+        assert (np.abs(host(out) - ref) <= tol).all()
+        ids, start = ragged(history, torch.int32)
+        logits = sg.adjust_logits(out.reshape(2, -1) @ head, history=ids, history_start=start, repetition=rep, masks=masks)
+        u = torch.tensor([0.2 + 0.15 * step, 0.9 - 0.1 * step], device="cuda")
+        t, p = torch.tensor([0.7, 1.1], device="cuda"), torch.full((2,), 0.9, device="cuda")
+        lp = torch.empty(2, device="cuda")
+        got = sg.sample(logits, u, temperature=t, top_k=ints([40, 0]), top_p=p, logprob=lp)
+        for b in range(2):
+            want = odec.sample(host(logits)[b], float(u[b]), float(t[b]), (40, 0)[b], float(p[b]))
+            assert want[2] > vocab * 2.0 ** -43 and int(got[b]) == want[0] and bool(allowed[b, int(got[b])])
+            assert abs(float(lp[b]) - want[1]) <= 2.0 ** -23 * abs(want[1]) + 2.0 ** -23
+        history = [h + [int(x)] for h, x in zip(history, got)]
+
+
+def test_captured_step_in_8_bits():
+    """The same four captured once and replayed while lengths and inputs change, eager calls in between."""
+    say("case graph 8")
+    heads, kv, dim, vocab = 8, 2, 128, 5000
+    s = Setup8([1, 1], [1, 1], 16, heads, kv, dim, F16, 19, per_seq=80, spare=200, block=16)
+    s.pages[:] = np.random.default_rng(20).permutation(160).reshape(2, 80)
+    s.seqs.pages.copy_(ints(s.pages))
+    rope, x = sg.Rope(dim), torch.randn(2, vocab, device="cuda").half()
+    u, p, rep = torch.rand(2, device="cuda"), torch.full((2,), 0.95, device="cuda"), torch.full((2,), 1.5, device="cuda")
+    hist, start = torch.zeros(64, dtype=torch.int32, device="cuda"), ints([0, 3, 9])
+    now = [t.view(torch.uint8) for t in (s.k8, s.v8, s.scales)]
+    first = [t.clone() for t in now]
+
+    def step():
+        q = s.cache.append(s.seqs, s.k, s.v, rope=rope, q=s.q)
+        logits = sg.adjust_logits(x, history=hist, history_start=start, repetition=rep)
+        return (s.cache.attend(s.seqs, q, max_ctx=1280), s.cache.attend(s.seqs, q, max_ctx=1280, window=200, sinks=4),
+                sg.sample(logits, u, top_p=p))
+
+    step()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph, other = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            out = step()
+        with torch.cuda.graph(other, stream=side):
+            out2 = step()
+    torch.cuda.synchronize()
+    for round_, ctx in enumerate([[1, 2], [17, 900], [1280, 64], [500, 1]]):
+        s.seqs.ctx_len.copy_(ints(ctx))
+        g = torch.Generator(device="cuda").manual_seed(round_)
+        for t in (s.q, s.k, s.v, x):
+            t.copy_(torch.randn(t.shape, device="cuda", generator=g))
+        u.copy_(torch.rand(2, device="cuda", generator=g))
+        hist.copy_(torch.randint(0, vocab, (64,), device="cuda", generator=g))
+        for t, t0 in zip(now, first):
+            t.copy_(t0)
+        eager = [t.clone() for t in step()]
+        cache = [t.clone() for t in now]
+        for t, t0 in zip(now, first):
+            t.copy_(t0)
+        for gr, o in ((graph, out), (other, out2), (graph, out)):
+            gr.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(o, eager))
+            assert all(torch.equal(a, b) for a, b in zip(now, cache))

@@ -115,6 +115,16 @@ def test_ties(vocab, dtype):
     check(both, [0.4, 0.8], top_k=[max(1, vocab // 2), 3])
 
 
+def test_largest_vocabulary():
+    """2^20 tokens: of equal logits the sums reach 2^63."""
+    say("case sample 2^20")
+    n = 1 << 20
+    check(torch.full((3, n), 7.25, dtype=F16, device="cuda"), [0.99999, 0.5, 0.1], top_p=[0.25, 1.0, 0.75], top_k=[0, 700000, n])
+    check(logits(2, n, BF16, 11), uniforms(2, 3), top_p=[0.7, 1.0], temperature=[1.1, 0.9])
+    with pytest.raises(sg.SgemvError):
+        sg.sample(torch.zeros(1, n + 1, device="cuda"), torch.zeros(1, device="cuda"))
+
+
 def test_special_values():
     say("case sample special values")
     inf, nan = math.inf, math.nan
