@@ -26,8 +26,20 @@ template <int DP> constexpr int kFewWaves = DP == 256 ? 4 : 8;
 //
 // EIGHT: the cache holds codes of 8 bits. A lane's 16 bytes of K are then 16
 // columns, 8 for each of two steps, so the columns of q go by them; the codes of
-// two of V's rows are put together before they are converted.
-// WINDOW: key numbers leave out what no row of the tile sees.
+// two of V's rows are put together before they are converted. A block's scale of
+// K goes to the scores (one factor for 4 keys), that of V into the conversion,
+// which takes it for nothing; sums are in units of the largest so far. Half the
+// bytes, and 382 vector instructions for a wave's 32 keys: with the same 128
+// columns, one row over 131071 slots of 8 heads takes 48.7 us and 4.7 of join
+// (head-major, 5.5 TB/s), 16 rows of 32 heads over up to 2500 slots 58 (3.6 TB/s;
+// head-major 47: a head's row is 128 bytes in 4 KiB else, and reads of 128 bytes
+// reach less). Tried: three blocks in flight (58.2 -> 59.5, 53.4 -> 54.5), two
+// workgroups a compute unit with one block each (58.2 -> 65.9), 4 waves (60), all
+// heads of a token in one XCD (59.3).
+//
+// WINDOW: key numbers leave out what no row of the tile sees. 16 rows of 8 heads
+// of 4 over a window of 4096 and 4 sinks of 60000 slots: 52.4 us and 4.8 of join,
+// 5.1 TB/s of the keys that are seen, as without a window over as many.
 template <class T, int DP, bool WHOLE, bool EIGHT, bool WINDOW>
 struct Few {
   using Elem = std::conditional_t<EIGHT, uint8_t, uint16_t>;

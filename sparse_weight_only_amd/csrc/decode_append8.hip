@@ -91,7 +91,14 @@ enum Pairing { kApart, kWithin, kAnyhow };
 // that every row is read once: the values stay in registers while the block's
 // largest magnitude is found in LDS. A rotated chunk reads its partner's columns
 // beside its own (from the same cache lines as the lane that has them).
-// Bound by memory; single tokens by their round trips.
+// Bound by memory: a batch of 5 prompts of up to 4001 tokens, 96 heads of 128
+// columns, blocks of 16, takes 150 us at 4.0 TB/s of the rows read and written
+// (copies reach 4.7 to 4.9). 16 single tokens: 5.0 us, the launch and two round
+// trips (a sequence's lengths and page, then its rows). The rows' loads are asked
+// for before the sines are worked out, which then cost nothing up to blocks of
+// 32; larger ones (64: 237 us, 128: 264) work out more of them in each workgroup
+// for fewer heads, and a rotated width whose halves are no whole chunks goes
+// column by column (40 of 128: 190).
 //
 // Blocks are numbered without a pass over the sequences: sequence s, whose
 // first new token is a, has the numbers from floor(a / B) + 2 s on; n tokens fall
@@ -371,7 +378,10 @@ extern "C" int sgemv_append8(const sgemv_cache8* cache, const sgemv_seqs* seqs, 
   p.groups = (most + kHold - 1) / kHold;
   // four waves, or as many as a head takes (a batch of prompts of up to 4001
   // tokens, 96 heads of 128 columns, blocks of 16: 149 us with 4 tokens a lane and
-  // 4 waves, 164 with 8 waves; 179 with 2 tokens; 191 with 8, 184 of them and 8 waves)
+  // 4 waves, 164 with 8 waves; 179 with 2 tokens; 191 with 8, 184 of them and 8 waves;
+  // 16 waves for blocks of more than 16: 32 slots 157 -> 166, 64 and 128 within 1 %.
+  // Sines of a quarter of the block at a time take less LDS, but a barrier each:
+  // 64 slots 237 -> 199, 16 of them 150 -> 162)
   p.lanes = p.chunks * p.groups > 256 ? (p.chunks * p.groups + 63) / 64 * 64 : 256;
   p.per = p.lanes / p.chunks / p.groups;
   const int64_t units = (k->tokens >> p.block_shift) + 2 * (int64_t)seqs->count;

@@ -30,8 +30,12 @@ constexpr int kBins = 2048;                          // of a step of a search
 constexpr int kMassBins = 512, kBinsPerPower = 16;   // of a wave's masses by value: 16 to a power of two
 constexpr int kHeld = 32;                            // logits that a lane may hold
 typedef float floats __attribute__((ext_vector_type(kHeld)));
-constexpr int kList = 8192;                          // tokens that are looked at one by one
-constexpr int kMostK = 768;                          // see candidates()
+constexpr int kList = 8192;                          // tokens that are looked at one by one: 64 KiB of places
+// The k-th largest of the lanes' own largest is a bound: where logits come in no
+// order 1024 ln(1024 / (1024 - k)) of a row are above it, 1420 for 768. From there
+// on the searches over the row are hardly slower (1 x 32000: top_k 50 8.2 us, 768
+// 18.6, 1000 30.2).
+constexpr int kMostK = 768;
 
 struct SampleParams {
   const void* x;
@@ -290,7 +294,10 @@ __device__ __forceinline__ uint64_t mass_from(Shared& s, const R& row, const S& 
   return all;
 }
 
-constexpr int kPairs = 256;                          // tokens that are compared each with each
+// Tokens that are compared each with each, 4 to 16 lanes a token: 64 comparisons a
+// lane at most, in place of a histogram's barriers (1 x 32000, top_k 50: 18 -> 12.6
+// us, 16 x 32000 with top_p: 35 -> 25).
+constexpr int kPairs = 256;
 
 // Up to kPairs places, each with all: for the lane that a token is with (one of 4
 // to 16 neighbours) its place and weight, its rank and the weight of those larger;
@@ -389,7 +396,22 @@ __device__ uint64_t find_border(Shared& s, const R& row, const S& source, uint64
 // sixteenth of it, that the sums of the kept p point at.
 //
 // HELD, for rows that fit: what a lane reads of its wave's stretch stays in its
-// registers, and the row is read once.
+// registers, and the row is read once (1 x 32000 among other calls, top_k 50 and
+// top_p: 10.3 -> 9.2 us).
+//
+// A row is bound by its round trips where there are few: 1 x 32000 takes 4.0 us
+// for the largest logit, 6.6 with min_p, 8.2 with top_k 50, 8.8 with top_p behind
+// it, 18 with top_p alone. Of 256 rows of 128003, one a compute unit, 29 us are
+// the pass over the logits (131 MB at 4.5 TB/s), 43 top_k, 50 min_p; top_p alone,
+// 80, is bound by the vector units: 26 us of 64-bit weights with an LDS atomic
+// each. Its rows are read 2.8 times: for the largest, the masses and the list,
+// and the list's pass takes 15 to 20 us although few of it are listed.
+// Searches over the row, which is what is left for top_k over 768 and flat rows,
+// take 120 there.
+//
+// LIGHT and HEAVY loads of a lane are on their way: 4 where a logit takes a few
+// operations, 2 of 16 bytes of FP32 where it takes a weight. With more the loops,
+// each gone through a few times, take longer to fetch than what they wait less.
 template <class T, int PER, bool HELD>
 __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
   __shared__ Shared s;
@@ -509,19 +531,22 @@ __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
     }
     row.least = of_key(yes);
   }
-  // lists the tokens from `bound` on that are wanted; how many there are
+  // lists the tokens from `bound` on that are wanted; how many there are, or more
+  // than the list takes
   const auto list = [&](float bound, auto wanted) {
+    bool full = false;                                 // to this lane's knowledge; a held row is soon through
     own(light, [&](const float (&v)[PER], int id) {
       // most lanes have none: one look at the largest
       float top = v[0];
 #pragma unroll
       for (int e = 1; e < PER; ++e) top = fmaxf(top, v[e]);
-      if (!(top >= bound)) return;
+      if (!(top >= bound) || (!HELD && full)) return;
       uint32_t bits = 0;
 #pragma unroll
       for (int e = 0; e < PER; ++e) bits |= (uint32_t)(v[e] >= bound && wanted(v[e])) << e;
       if (!bits) return;
       int at = atomicAdd(&s.listed, __popc(bits));
+      if (!HELD) full = at >= kList;
       while (bits) {
         const int e = __ffs(bits) - 1;
         bits &= bits - 1;

@@ -42,7 +42,7 @@ def check(x, uniform, temperature=None, top_k=None, top_p=None, min_p=None):
     for r in range(rows):
         for again in range(20):
             a = odec.sample(x64[r], float(uniform[r]), float(t[r]), int(k[r]), float(tp[r]), float(mp[r]))
-            if a[2] == 0 or a[2] > (vocab + 1) * 2.0 ** -43 or not 0 < uniform[r] < 1:
+            if a[2] == 0 or a[2] > (vocab + 1) * 2.0 ** -43 or not 0 < uniform[r] < 1 or again == 19:
                 break                                   # 0: equal weights, whose sums are exact on both sides
             uniform[r] = np.float32((uniform[r] + 0.3819) % 1.0)
         ref.append(a)
@@ -113,6 +113,17 @@ def test_ties(vocab, dtype):
     both = torch.zeros(2, vocab, device="cuda")
     both[:, ::2] = -0.0
     check(both, [0.4, 0.8], top_k=[max(1, vocab // 2), 3])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
+@pytest.mark.parametrize("vocab", [8193, 32761, 50021])
+def test_more_than_are_listed(vocab, dtype):
+    # min_p leaves thousands of tokens: with top_p, with many of the largest, and alone
+    say("case sample long lists", vocab, dtype)
+    x, u = logits(6, vocab, dtype, vocab, peaks=0), uniforms(6, vocab + 1)
+    check(x, u, min_p=[1e-7] * 6)
+    check(x, u, min_p=[1e-7] * 6, top_p=[0.3, 0.6, 0.9, 0.97, 0.99, 0.5])
+    check(x, u, min_p=[1e-7] * 6, top_k=[5000, 8192, 2000, 769, 40, 8000], temperature=[0.5, 3.0, 20.0, 1.0, 1.0, 100.0])
 
 
 def test_largest_vocabulary():
