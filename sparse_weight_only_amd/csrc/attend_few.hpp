@@ -30,8 +30,8 @@ template <int DP> constexpr int kFewWaves = DP == 256 ? 4 : 8;
 // K goes to the scores (one factor for 4 keys), that of V into the conversion,
 // which takes it for nothing; sums are in units of the largest so far. Half the
 // bytes, and 382 vector instructions for a wave's 32 keys: with the same 128
-// columns, one row over 131071 slots of 8 heads takes 48.7 us and 4.7 of join
-// (head-major, 5.5 TB/s), 16 rows of 32 heads over up to 2500 slots 58 (3.6 TB/s;
+// columns, one row over 131071 slots of 8 heads takes 53 us with its join (head-major;
+// 5.1 TB/s), 16 rows of 32 heads over up to 2500 slots 58 (3.6 TB/s;
 // head-major 47: a head's row is 128 bytes in 4 KiB else, and reads of 128 bytes
 // reach less). Tried: three blocks in flight (58.2 -> 59.5, 53.4 -> 54.5), two
 // workgroups a compute unit with one block each (58.2 -> 65.9), 4 waves (60), all

@@ -92,7 +92,7 @@ enum Pairing { kApart, kWithin, kAnyhow };
 // largest magnitude is found in LDS. A rotated chunk reads its partner's columns
 // beside its own (from the same cache lines as the lane that has them).
 // Bound by memory: a batch of 5 prompts of up to 4001 tokens, 96 heads of 128
-// columns, blocks of 16, takes 150 us at 4.0 TB/s of the rows read and written
+// columns, blocks of 16, takes 150 us at 3.8 TB/s of the rows read and written
 // (copies reach 4.7 to 4.9). 16 single tokens: 5.0 us, the launch and two round
 // trips (a sequence's lengths and page, then its rows). The rows' loads are asked
 // for before the sines are worked out, which then cost nothing up to blocks of
