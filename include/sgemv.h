@@ -571,9 +571,11 @@ int sgemv_append8(const sgemv_cache8* cache, const sgemv_seqs* seqs, const sgemv
  * without one that a token of it can see.
  * Numerics: codes are exact in the queries' type; each p_t is rounded to it as in
  * sgemv_attend, so |out - exact| is within the bound given there. In BF16 values
- * in blocks of exponents up to -96 may count as 0 beside others. A score is
- * summed in FP32 in units of its block's scale, so q times the codes must not
- * overflow (no query below 2^100 does). */
+ * in blocks of exponents up to -96 may count as 0 beside others (of K where
+ * queries go beyond 2^16 or `scale` leaves no score of such keys over 2^-26), in
+ * either type keys of a scale byte of 0. A score is summed in FP32 in units of
+ * its block's scale, so q times the codes must not overflow (no query below 2^100
+ * does). */
 int sgemv_attend8_plan(const sgemv_cache8* cache, const sgemv_seqs* seqs, int32_t tokens, int32_t heads, int32_t window, int32_t sinks,
                        int32_t max_ctx, sgemv_attend_plan_t* out);
 int sgemv_attend8(const sgemv_cache8* cache, const sgemv_seqs* seqs, const sgemv_rows* q, const sgemv_rows* out, float scale,

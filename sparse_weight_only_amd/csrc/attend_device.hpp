@@ -97,24 +97,32 @@ template <> struct Half<__bf16> {
 // Where exponents differ by more than kSpread the tile is summed again key by
 // key in FP32, so that a row is as exact as its own keys allow whatever other
 // rows of its tile see. Exponents up to kTiny do not count for that: FP16
-// results below 2^-25 are 0 (values up to 448 2^-35; of K up to kTinyKey, since
-// any q leaves a score of such keys under 2^-26); in BF16 they are those that an
-// append gives to zeros.
+// results below 2^-25 are 0 (values up to 448 2^-35); in BF16 they are those that
+// an append gives to zeros. Of K those up to tiny_key() do not.
 template <class T> struct Eight;
 template <> struct Eight<_Float16> {
-  static constexpr int kSpread = 15, kTiny = 127 - 35, kTinyKey = 127 - 60;
+  static constexpr int kSpread = 15, kTiny = 127 - 35;
   static __device__ __forceinline__ uint32_t pair(uint32_t codes, float scale, bool high) {
     return high ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes, scale, true))
                 : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes, scale, false));
   }
 };
 template <> struct Eight<__bf16> {
-  static constexpr int kSpread = 60, kTiny = 127 - 96, kTinyKey = 127 - 96;
+  static constexpr int kSpread = 60, kTiny = 127 - 96;
   static __device__ __forceinline__ uint32_t pair(uint32_t codes, float scale, bool high) {
     return high ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, scale, true))
                 : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, scale, false));
   }
 };
+// The largest exponent (biased) of keys that no score can tell from zeros: 256
+// products of a query up to 2^16 and a key up to 448 2^e, times scale2 < 2^(s + 1),
+// stay below 2^-26 for e <= -60 - s. In BF16 no more than kTiny, which goes down
+// with larger scales too (s > 36); 0 always, which keys that are not there have.
+template <class T>
+__device__ __forceinline__ int tiny_key(float scale2) {
+  const int s = (int)(__builtin_bit_cast(uint32_t, scale2) >> 23) - 127, e = 127 - 60 - (s > 0 ? s : 0);
+  return e < 0 ? 0 : e < Eight<T>::kTiny ? e : Eight<T>::kTiny;
+}
 // 8 codes as 8 halves
 template <class T>
 __device__ __forceinline__ dword4 eight(uint32_t lo, uint32_t hi, float scale) {

@@ -79,6 +79,7 @@ struct Many {
   // EIGHT (exponents are biased): what `o` is in units of; the largest of K and
   // of V so far, which is what LDS holds a block in units of; the least that count
   int unit, k_top, v_top, k_least, v_least;
+  int k_tiny;                                            // and up to where those of K do not
 
   __device__ __forceinline__ Many(const AttendParams& p_, const Tile& t_, int head, uint16_t* lds_) : p(p_), t(t_), lds_p(lds_) {
     lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint16_t*)lds_;
@@ -379,14 +380,14 @@ struct Many {
     const int key = lane / ROW_LANES, d = lane % ROW_LANES * CP;
     {
       const int ek = x.e & 255u, ev = x.e >> 8;
-      const bool news = ek > k_top || ev > v_top || (ek > Eight<T>::kTinyKey && ek < k_least) || (ev > Eight<T>::kTiny && ev < v_least);
+      const bool news = ek > k_top || ev > v_top || (ek > k_tiny && ek < k_least) || (ev > Eight<T>::kTiny && ev < v_least);
       if (__any(news)) {
 #pragma unroll 1
         for (int g = 0; g < GROUPS; ++g) {
           const int e = __builtin_amdgcn_readlane(x.e, g), gk = e & 255, gv = e >> 8;
           k_top = gk > k_top ? gk : k_top;
           v_top = gv > v_top ? gv : v_top;
-          k_least = gk > Eight<T>::kTinyKey && gk < k_least ? gk : k_least;
+          k_least = gk > k_tiny && gk < k_least ? gk : k_least;
           v_least = gv > Eight<T>::kTiny && gv < v_least ? gv : v_least;
         }
       }
@@ -501,6 +502,7 @@ struct Many {
     l = 0.0f;
     unit = k_top = v_top = 0;
     k_least = v_least = 255;
+    k_tiny = tiny_key<T>(p.scale2);
 #pragma unroll
     for (int i = 0; i < OT; ++i) o[i] = f32x16{};
     if (t.key0 >= t.key1 || p.seq.n_pages == 0) return;

@@ -376,6 +376,27 @@ def test_attend8_exponents_far_apart(n, ctx, dim, dtype, far):
         assert (np.abs(got[i] - out[i]) <= tol).all(), (i, (np.abs(got[i] - out[i]) - tol).max())
 
 
+# rows of the many-row kernel: full tiles, and 128 rows of them (room for more than 4096 slots)
+@pytest.mark.parametrize("n,dim,per", [(300, 64, None), (60, 64, 600), (300, 128, None), (60, 128, 600), (300, 256, None)])
+@pytest.mark.parametrize("dtype,least,far,scale", [(F16, -62, 40, 2.0 ** 52), (F16, -75, 35, 2.0 ** 65), (BF16, -96, 130, 2.0 ** 86),
+                                                   (BF16, -70, 10, 2.0 ** 60)])
+def test_attend8_small_keys_under_a_large_scale(n, dim, per, dtype, least, far, scale):
+    """Keys of the smallest scales, whose scores count since `scale` is large, in one block with keys of larger ones
+    that only later rows see."""
+    say("case attend8 large scale", n, dim, per, dtype, least, far, scale)
+    s = Setup8([n], [n], 16, 2, 1, dim, dtype, 16, block=8, per_seq=per)
+    assert s.cache.plan(s.seqs, n, 2).tile_rows == (128 if per and dim <= 128 else 256)
+    late = 56                                              # slots 56 to 63 have the larger ones
+    s.scales.view(torch.uint8)[..., 0] = 127 + least
+    s.scales.view(torch.uint8)[s.pages[0, late // 16], late % 16 // 8, :, 0] = 127 + least + far
+    if dtype == BF16:
+        s.q[late:] *= 2.0 ** -60                           # scores that FP32 holds
+    s.values()
+    want = s.want(scale)
+    assert want[2][:late].max() < 200                      # scores of a few units: their rows' tolerances are those of roundings
+    s.check(s.cache.attend(s.seqs, s.q, scale=scale), want, f"{n} {dim} {dtype}")
+
+
 # room for more than 4096 slots a sequence, which the launch goes by: the kernel for many rows, in its form for few tokens
 ROOMY = [([60], [300], 16, 2, 1, 64, F16, 600), ([27, 33], [1100, 90], 16, 4, 2, 128, F16, 600), ([40], [40], 8, 3, 1, 128, BF16, 700),
          ([25, 30], [2000, 1025], 8, 8, 2, 80, F16, 700), ([20], [1200], 16, 4, 1, 256, F16, 400), ([60, 1, 0], [200, 3000, 7], 128, 3, 3, 96, BF16, 60),
