@@ -29,8 +29,9 @@ def asan_runtime() -> str:
                           check=True).stdout.strip()
 
 
-# The decode-step operators' index arithmetic (csrc/decode_index.hpp, shared
-# with the kernels) as programs of their own for the CPU tests.
+# The decode-step operators' index arithmetic (csrc/decode_index.hpp and
+# sample_bound.hpp, shared with the kernels) as programs of their own for the
+# CPU tests.
 _INDEX_DIR = os.path.join(os.path.dirname(os.path.dirname(CSRC)), "tests", "decode_index")
 INDEX_SRC = os.path.join(_INDEX_DIR, "index_check.cpp")
 INDEX_CHECK = os.path.join(_INDEX_DIR, "_build", "index_check")
@@ -38,11 +39,13 @@ VISIBLE_SRC = os.path.join(_INDEX_DIR, "visible_check.cpp")
 VISIBLE_CHECK = os.path.join(_INDEX_DIR, "_build", "visible_check")
 WINDOW_SRC = os.path.join(_INDEX_DIR, "window_check.cpp")
 WINDOW_CHECK = os.path.join(_INDEX_DIR, "_build", "window_check")
+BOUND_SRC = os.path.join(_INDEX_DIR, "bound_check.cpp")
+BOUND_CHECK = os.path.join(_INDEX_DIR, "_build", "bound_check")
 
 
 def build_index_check(verbose: bool = False) -> str:
     os.makedirs(os.path.dirname(INDEX_CHECK), exist_ok=True)
-    for src, exe in ((INDEX_SRC, INDEX_CHECK), (VISIBLE_SRC, VISIBLE_CHECK), (WINDOW_SRC, WINDOW_CHECK)):
+    for src, exe in ((INDEX_SRC, INDEX_CHECK), (VISIBLE_SRC, VISIBLE_CHECK), (WINDOW_SRC, WINDOW_CHECK), (BOUND_SRC, BOUND_CHECK)):
         tmp = exe + ".tmp"
         _run(["g++", "-std=c++17", "-O1", "-g", "-fno-omit-frame-pointer", "-fsanitize=address,undefined",
               "-fno-sanitize-recover=all", "-Wall", "-Wextra", src, "-o", tmp], verbose)

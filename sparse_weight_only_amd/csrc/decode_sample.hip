@@ -18,12 +18,19 @@
 
 #include "decode_internal.hpp"
 #include "launch_util.hpp"
+#include "sample_bound.hpp"
 
 using namespace sgemv;
 
 namespace {
 
-constexpr int kLanes = 1024, kWaves = kLanes / 64;
+using sgemv_dev::KeyBins;
+using sgemv_dev::LogitBins;
+using sgemv_dev::key_of;
+using sgemv_dev::of_key;
+
+constexpr int kLanes = sgemv_dev::kSampleLanes, kWaves = sgemv_dev::kSampleWaves;
+constexpr uint32_t kNever = sgemv_dev::kNeverKey;
 constexpr int kUnit = 43;                            // p in units of 2^-43: 2^20 of them fit 64 bits
 constexpr int kMostVocab = 1 << 20;
 constexpr int kBins = 2048;                          // of a step of a search
@@ -32,9 +39,9 @@ constexpr int kHeld = 32;                            // logits that a lane may h
 typedef float floats __attribute__((ext_vector_type(kHeld)));
 constexpr int kList = 8192;                          // tokens that are looked at one by one: 64 KiB of places
 // The k-th largest of the lanes' own largest is a bound: where logits come in no
-// order 1024 ln(1024 / (1024 - k)) of a row are above it, 1420 for 768. From there
-// on the searches over the row are hardly slower (1 x 32000: top_k 50 8.2 us, 768
-// 18.6, 1000 30.2).
+// order and every lane has some, 1024 ln(1024 / (1024 - k)) of a row are above it,
+// 1420 for 768. From there on the searches over the row are hardly slower (1 x
+// 32000: top_k 50 8.2 us, 768 18.6, 1000 30.2).
 constexpr int kMostK = 768;
 
 struct SampleParams {
@@ -47,15 +54,6 @@ struct SampleParams {
   float* logprob;
   int32_t vocab;
 };
-
-// Whole numbers in the order of the floats; both zeros the same, NaN as -inf.
-__device__ __forceinline__ uint32_t key_of(float x) {
-  x = x != x ? -__builtin_inff() : x + 0.0f;
-  const uint32_t b = __builtin_bit_cast(uint32_t, x);
-  return b >> 31 ? ~b : b | 0x80000000u;
-}
-__device__ __forceinline__ float of_key(uint32_t k) { return __builtin_bit_cast(float, k >> 31 ? k & 0x7fffffffu : ~k); }
-constexpr uint32_t kNever = 0x007fffffu;             // the key of -inf
 
 // A token's place in its row's order by value, the largest first: of equal
 // logits the lower id.
@@ -384,8 +382,13 @@ __device__ uint64_t find_border(Shared& s, const R& row, const S& source, uint64
 
 // One workgroup a row. Ways to what is kept:
 //  * top_k up to kMostK: at least k tokens are as large as the k-th largest of the
-//    lanes' own largest logits, and hardly more; those are listed. With min_p
-//    those that it leaves are.
+//    lanes' own largest logits, and hardly more; those are listed, and up to 64
+//    lanes' more, since the k-th is looked for by counting (sample_bound.hpp).
+//    Lanes without a logit, which many lengths and masks leave, do not count (1 x
+//    50257 in 16 bits, top_k 50: 11 us, 44 with all of the row listed); tokens
+//    of -1e9 in place of -inf cost two counts more (1 x 32000, 90 % of them: 11.4
+//    us, 9.1 without). All are listed where fewer than k lanes have any. With min_p
+//    alone those that it leaves are.
 //  * top_p without them, or more than the list takes: each wave sums the p of its
 //    stretch of the row by value, in bins of 1/16 power of two; the tokens of the
 //    bin that the border falls into are listed.
@@ -424,7 +427,7 @@ __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
   const float top_p = p.top_p ? p.top_p[r] : 1.0f, min_p = p.min_p ? p.min_p[r] : 0.0f;
   constexpr int LIGHT = 4, HEAVY = PER == 1 ? 2 : 8 / PER;   // loads on their way
   // a wave's stretch of the row, in whole steps of the wave
-  const int stretch = (row.vocab + kWaves * 64 * PER - 1) / (kWaves * 64 * PER) * (64 * PER);
+  const int stretch = sgemv_dev::stretch_of(row.vocab, PER);
   const int from = wave * stretch < row.vocab ? wave * stretch : row.vocab, to = from + stretch < row.vocab ? from + stretch : row.vocab;
   if (tid < kWaves) s.stretch[tid] = 0;
   if (tid == 0) s.listed = 0;
@@ -473,7 +476,7 @@ __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
   row.scale = 1.4426950408889634074 / (double)t;
   const double log_p = min_p > 0.0f && min_p < 1.0f ? log2((double)min_p) : 0.0;
   const uint32_t mine = key_of(most);
-  uint32_t top_key = mine, low_key = ~mine;            // of the lanes' largest the largest and the smallest
+  uint32_t top_key = mine, low_key = sgemv_dev::low_part(mine);   // of the lanes' largest the largest and the smallest
   block_max(s, top_key, low_key);
   low_key = ~low_key;
   if (top_key <= kNever) {
@@ -566,20 +569,44 @@ __global__ void __launch_bounds__(kLanes) sample_kernel(SampleParams p) {
   if (by_count || (some && k <= 0)) {
     float bound = row.least;
     if (by_count) {
-      // the bin of the k-th largest of the lanes' largest, of kLanes bins between
-      // the smallest and the largest of them; all where not so many lanes have any
-      const float by = (float)kLanes / (row.top - fmaxf(of_key(low_key), -0x1.fffffep127f));
-      if (most >= row.least) atomicAdd(&s.count[(int)fminf(fmaxf((row.top - most) * by, 0.0f), kLanes - 1.0f)], 1u);   // no number (0 by infinity): 0
+      // the interval of the k-th largest of the lanes' largest; none where not so many lanes have any
+      bool here = most >= row.least;
+      const auto find = [&](int at, int need) {
+        if (here) atomicAdd(&s.count[at], 1u);
+        __syncthreads();
+        uint32_t all;
+        const uint32_t c = s.count[tid], before = block_prefix(s, c, all);
+        s.count[tid] = 0;
+        if (before < (uint32_t)need && before + c >= (uint32_t)need) {
+          s.bin = tid;
+          s.above = before;
+          s.bin_count = c;
+        }
+        __syncthreads();
+      };
       if (tid == 0) s.bin = kLanes;
-      __syncthreads();
-      uint32_t all;
-      const uint32_t c = s.count[tid], before = block_prefix(s, c, all);
-      if (before < (uint32_t)k && before + c >= (uint32_t)k) s.bin = tid;
-      __syncthreads();
-      // its lower end, less what the roundings there and here may come to
-      const float end = row.top - (s.bin + 1.0f) / by;
-      const float lower = end - (__builtin_fabsf(row.top) + __builtin_fabsf(end)) * 0x1p-20f;
-      if (s.bin < kLanes - 1 && lower > bound) bound = lower;
+      const LogitBins bins(row.top, fmaxf(of_key(low_key), row.least));
+      int at = bins.bin(most), need = k;
+      find(at, need);
+      if (s.bin < kLanes) {
+        bound = fmaxf(bound, bins.lower(s.bin));
+        if (s.bin_count > (uint32_t)sgemv_dev::kCrowd) {
+          here &= at == s.bin;
+          need -= (int)s.above;
+          uint32_t hi = here ? mine : 0, lo = here ? ~mine : 0;
+          block_max(s, hi, lo);
+          KeyBins keys(hi, ~lo);
+          for (int round = 0; round < sgemv_dev::kKeyRounds; ++round) {
+            at = here ? keys.bin(mine) : 0;
+            find(at, need);
+            here &= at == s.bin;
+            need -= (int)s.above;
+            keys.narrow(s.bin);
+            if (s.bin_count <= (uint32_t)sgemv_dev::kCrowd || keys.low == keys.top) break;
+          }
+          bound = fmaxf(bound, of_key(keys.low));
+        }
+      }
     }
     n = list(bound, [](float) { return true; });
   }

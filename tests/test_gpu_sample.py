@@ -126,6 +126,29 @@ def test_more_than_are_listed(vocab, dtype):
     check(x, u, min_p=[1e-7] * 6, top_k=[5000, 8192, 2000, 769, 40, 8000], temperature=[0.5, 3.0, 20.0, 1.0, 1.0, 100.0])
 
 
+@pytest.mark.parametrize("vocab", [5003, 30522, 32000, 50257, 100277])
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+def test_top_k_where_lanes_have_no_logit(vocab, dtype):
+    """Lengths and masks that leave some lanes without a token, or with none but far ones."""
+    say("case sample empty lanes", vocab, dtype)
+    far = -6e4 if dtype == F16 else -1e9
+    x = logits(9, vocab, dtype, vocab + 1)
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    some = torch.rand(9, vocab, device="cuda", generator=g)
+    x[1, : vocab // 2] = -math.inf
+    x[2].masked_fill_(some[2] < 0.9, -math.inf)
+    x[3].masked_fill_(some[3] < 0.9, far)
+    x[4].masked_fill_(some[4] < 0.95, torch.finfo(dtype).min)
+    x[5, -vocab // 30:] = far
+    x[6] = (-10.0 ** (torch.arange(vocab, device="cuda") % (4 if dtype == F16 else 38))).to(dtype).where(some[6] < 0.5, x[6])
+    x[7].masked_fill_(some[7] < 0.9, math.nan)
+    x[8] -= 4000.0
+    for k in (1, 50, 300, 768):
+        check(x, uniforms(9, k), top_k=[k] * 9)
+        check(x, uniforms(9, k + 1), top_k=[k] * 9, top_p=[0.9] * 9, temperature=[1.5] * 9)
+    check(x, uniforms(9, 9), top_k=[50] * 9, min_p=[1e-4] * 9)
+
+
 def test_largest_vocabulary():
     """2^20 tokens: of equal logits the sums reach 2^63."""
     say("case sample 2^20")

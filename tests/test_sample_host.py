@@ -2,13 +2,15 @@
 point refuses before any HIP call."""
 import ctypes
 import math
+import os
+import subprocess
 
 import numpy as np
 import pytest
 
 import sparse_weight_only_amd as sg
 from oracle import decode as odec
-from sparse_weight_only_amd import decode as D
+from sparse_weight_only_amd import _build, decode as D
 from sparse_weight_only_amd.sgemv import SGEMV_EALIGN, SGEMV_EINVAL, SGEMV_ESIZE
 from test_decode_host import BASE
 
@@ -40,6 +42,17 @@ def test_oracle_special_values():
     assert odec.sample([math.nan, 1.0, NO], 0.9)[:2] == (1, 0.0)
     assert odec.sample([math.inf, 1.0, math.inf], 0.6)[0] == 2 and odec.sample([math.inf, 1.0, math.inf], 0.4)[0] == 0
     assert odec.sample([0.0, -0.0, 0.0], 0.9, top_k=2)[0] == 1 and odec.sample([-1.0, 3.0, 3.0], 0.1, temperature=0.0)[0] == 1
+
+
+def test_bound_of_top_k_under_sanitizers():
+    """What is listed for top_k stays near k, whatever a row's length leaves without a logit, and whatever masks do."""
+    from sparse_weight_only_amd import _build_san
+    exe = _build_san.BOUND_CHECK
+    newest = max(os.path.getmtime(f) for f in [_build_san.BOUND_SRC] + [os.path.join(_build.CSRC, h) for h in ("sample_bound.hpp", "decode_index.hpp")])
+    if not os.path.exists(exe) or os.path.getmtime(exe) < newest:
+        _build_san.build_index_check()
+    r = subprocess.run([exe], stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.startswith("ok"), r.stdout[-3000:]
 
 
 def args(**kw):
