@@ -335,6 +335,55 @@ def test_attend8_unseen_slots_have_no_part(n, ctx, heads, kv):
     assert not torch.isnan(got).any() and not torch.isnan(plain).any()
 
 
+# the few-row kernel, its short tiles of more rows, tiles of 128 rows (windows of more than its 2048 or 4096 slots) and of 256
+HIDDEN = [(1, 300, 2, 2, 64, 50, 9), (3, 1500, 4, 2, 128, 50, 9), (60, 200, 2, 1, 64, 50, 9), (30, 2700, 2, 1, 64, 2100, 5),
+          (25, 5200, 4, 1, 128, 4300, 40), (90, 1200, 4, 2, 128, 50, 9), (300, 700, 1, 1, 256, 200, 70), (150, 900, 2, 1, 64, 100, 0)]
+
+
+@pytest.mark.parametrize("n,ctx,heads,kv,dim,window,sinks", HIDDEN)
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("kind,dtype", [(Setup, F16), (Setup, BF16), (Setup8, F16)])
+def test_what_a_window_hides_has_no_part(n, ctx, heads, kv, dim, window, sinks, tree, kind, dtype):
+    """Not numbers and infinities in every slot that no token sees, then anything in the table's entries of pages without another."""
+    say("case hidden", n, ctx, window, sinks, tree, kind.__name__, dtype)
+    s = kind([n], [ctx], 16, heads, kv, dim, dtype, 23, spare=3)
+    old, bits = ctx - n, None
+    low = old + 1 - window
+    if tree:
+        bits = np.zeros((n, (n + 31) // 32), np.uint32)
+        path = []
+        for i in range(n):
+            up, j = {i}, i
+            while j:
+                j = (j - 1) // 2
+                up.add(j)
+            for j in up:
+                bits[i, j // 32] |= np.uint32(1) << np.uint32(j % 32)
+            path.append(len(up))
+        low = min(old, old + min(path) - window)
+    hide = np.ones((s.n_pages, 16), bool)
+    for t in list(range(max(low, 0), ctx)) + list(range(min(sinks, ctx))):
+        hide[s.pages[0, t // 16], t % 16] = False
+    at = torch.from_numpy(hide).cuda()
+    if kind is Setup8:
+        for c in (s.k8, s.v8):
+            c.view(torch.uint8)[at] = 0x7F
+        clean = [np.nan_to_num(host(x)) for x in (s.kc, s.vc)]
+    else:
+        clean = [host(x) for x in (s.kc, s.vc)]
+        odd = torch.tensor([float("nan"), float("inf"), -float("inf")], device="cuda", dtype=dtype)
+        for c in (s.kc, s.vc):
+            c[at] = odd[torch.randint(0, 3, c[at].shape, device="cuda")]
+    want = odec.attend(host(s.q), *clean, s.new_start, s.ctx, s.pages, dim ** -0.5, bits, window, sinks)
+    kw = dict(tree=None if bits is None else ints(bits.view(np.int32)), window=window, sinks=sinks)
+    s.check(s.cache.attend(s.seqs, s.q, **kw), want, "hidden slots")
+    pages = s.pages.copy()
+    gone = [i for i in range(pages.shape[1]) if 16 * i >= sinks and 16 * (i + 1) <= low]
+    pages[0, gone] = np.resize([-1, s.n_pages, 2 ** 31 - 1, -2 ** 31, s.unused[0]], len(gone))
+    s.seqs.pages.copy_(ints(pages))
+    s.check(s.cache.attend(s.seqs, s.q, **kw), want, "pages given back")
+
+
 @pytest.mark.parametrize("n,ctx", [([1], [40]), ([20], [300]), ([150], [400])])
 def test_attend8_nan_that_is_seen(n, ctx):
     say("case attend8 NaN", n, ctx)
