@@ -22,6 +22,7 @@ from .sgemv import SgemvError, _check, _ptr, lib, SGEMV_EALIGN, SGEMV_EINVAL, SG
 
 F16, BF16, F32 = 0, 1, 2
 _P, _I32, _I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+_ALL = 2 ** 31 - 1                       # of slots: more than there can be
 
 
 class Rows(ctypes.Structure):
@@ -166,6 +167,14 @@ def _rows(x, what: str) -> bytes:
     return _pack_rows(x.data_ptr(), st, sh, t, h, d, dtype)
 
 
+def _slots(window: int, sinks: int):
+    """Numbers of slots as the C ABI takes them. ctypes would keep the low 32 bits of larger ones, which are more than any
+    context has, and of negative ones, which the library refuses."""
+    if 0 <= window <= _ALL and 0 <= sinks <= _ALL:
+        return window, sinks
+    return tuple(max(-1, min(n, _ALL)) for n in (window, sinks))
+
+
 def _on(device, **tensors) -> None:
     # a call asks each tensor's get_device() first, at half the cost, and comes here to say which one differs
     for what, x in tensors.items():
@@ -295,7 +304,7 @@ class PagedCache:
         """The entry points of an attention, and what they take behind the arguments that all have."""
         L = lib()
         if window or sinks:
-            return L.sgemv_attend_window_plan, L.sgemv_attend_window, (window, sinks), "sgemv_attend_window"
+            return L.sgemv_attend_window_plan, L.sgemv_attend_window, _slots(window, sinks), "sgemv_attend_window"
         return L.sgemv_attend_plan, L.sgemv_attend, (), "sgemv_attend"
 
     def append(self, seqs: Sequences, k, v, rope: Rope = None, q=None, q_out=None, positions=None, stream=None):
@@ -440,7 +449,7 @@ class PagedCache8(PagedCache):
 
     def _attend(self, window, sinks):
         L = lib()
-        return L.sgemv_attend8_plan, L.sgemv_attend8, (window, sinks), "sgemv_attend8"
+        return L.sgemv_attend8_plan, L.sgemv_attend8, _slots(window, sinks), "sgemv_attend8"
 
 
 def adjust_logits(x, out=None, history=None, history_start=None, prompt_len=None, repetition=None, frequency=None,

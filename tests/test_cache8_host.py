@@ -206,6 +206,25 @@ def test_plans():
 
 # ---------------------------------------------------------------- binding
 
+def test_windows_past_32_bits_are_not_cut():
+    """A window or sinks of more than 32 bits is all there is, and one far below 0 is refused, not what its low bits say."""
+    s = sg.Sequences(*(torch.zeros(n, dtype=torch.int32) for n in ((2,), (1,), (1, 40960))))
+    for cache_ in (sg.PagedCache(4, 16, 2, 64, device="cpu"), sg.PagedCache8(4, 16, 2, 64, device="cpu")):
+        def splits(**kw):
+            return cache_.plan(s, 1, 2, **kw).splits
+        whole = splits(window=2 ** 31 - 1)
+        assert whole == splits() > splits(window=5)
+        for n in (2 ** 31, 2 ** 32 + 5, 10 ** 30):
+            assert splits(window=n) == splits(window=5, sinks=n) == whole, n
+            for kw in (dict(window=-n), dict(window=5, sinks=-n), dict(sinks=n)):
+                with pytest.raises(sg.SgemvError) as e:
+                    splits(**kw)
+                assert e.value.code == SGEMV_EINVAL
+        for seen in ((2 ** 32 + 5, 0), (7, 2 ** 32), (-2 ** 32 + 5, 0)):      # what attend() passes on is what plan() does
+            given = cache_._attend(*seen)[2]
+            assert all(-2 ** 31 <= g < 2 ** 31 and (g < 0) == (n < 0) and (g == n or abs(n) >= 2 ** 31) for g, n in zip(given, seen))
+
+
 def test_binding_refuses_what_it_cannot_pass_on():
     b8 = lambda *shape: torch.zeros(shape, dtype=torch.uint8).view(torch.float8_e4m3fn)    # noqa: E731
     e8 = lambda *shape: torch.zeros(shape, dtype=torch.uint8).view(torch.float8_e8m0fnu)   # noqa: E731
