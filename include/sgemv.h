@@ -515,7 +515,9 @@ int sgemv_attend(const sgemv_cache* cache, const sgemv_seqs* seqs, const sgemv_r
 
 /* sgemv_attend_window - sgemv_attend through a sliding window: a token at slot
  * a sees slot t <= a where t > a - window (itself and the window - 1 before it)
- * or t < sinks (the first tokens of its sequence stay visible).
+ * or t < sinks (the first tokens of its sequence stay visible). Slots are
+ * counted, not positions: keys keep the positions that they were stored at, so
+ * behind a long stream the sinks are turned as far away as they lie.
  *   window : >= 1; 0 for none, as sgemv_attend (sinks must be 0 then).
  *   sinks  : >= 0.
  * With a tree a token sees new tokens by its bits alone, however many, and the
@@ -647,7 +649,8 @@ typedef struct sgemv_sampling {
  * Logits of +inf share the row alone. uniform outside [0, 1) counts as 0 or as
  * the largest number below 1.
  * Numerics: exponents and exponentials in 64 bits, p in whole multiples of
- * 2^-43 and so summed exactly, in any order: the same tokens on every call.
+ * 2^-43 and so summed exactly, in any order: the same tokens on every call. Tokens
+ * of less than 2^-44 weigh nothing, in top_p's sums too.
  * Enqueues one kernel and returns without synchronising.
  * Errors: EINVAL, EALIGN, ESIZE (vocab over 2^20, over 65535 rows), EHIP. */
 int sgemv_sample(const sgemv_sampling* s, void* hip_stream);

@@ -74,6 +74,12 @@ int make_shape(const Cache* c, const sgemv_seqs* s, int32_t tokens, int32_t head
   // against 33.3; 1 x 128 rows over 4000: 16.9 against 26.5). Through a window in
   // 16 bits up to 2048 (4 x 96 rows, a window of 1000: 16.1 against 24.3, of 2000:
   // 25.8 against 25.5, of 3000: 35.3 against 27.7; 1 x 128, of 2000: 15.8, 22.5).
+  // All these leave compute units without work. Where sequences and heads fill the
+  // chip tiles of 16 rows stay ahead over 8 bits up to 32 rows (16 and 64 sequences,
+  // 32 heads, 2000 slots: 85 against 106 us, 387 against 424) but not with 108, whose
+  // keys they read and convert seven times (4, 16 and 64 sequences: 73 against 49,
+  // 264 against 129, 1044 against 525; 64 over 500: 505 against 216): the rule does
+  // not look at that.
   const int64_t near = c->exps ? 4096 : c->window > 0 ? 2048 : 1024;
   h.few = rows <= (int64_t)16 * s->count || (rows <= (int64_t)128 * s->count && ctx <= near);
   h.waves = !h.few ? sgemv_dev::kManyWaves : h.dp == 256 ? sgemv_dev::kFewWaves<256> : sgemv_dev::kFewWaves<128>;

@@ -43,7 +43,8 @@ template <int DP> constexpr int kManyLds = kManyStages * 2 * kManyBlock<DP> * DP
 // third to the vector instructions: a prompt of 8192 and 32 heads of 128 columns
 // takes 616 us where 16 bits take 594 (matrix cores busy 40 % and 54 % of the
 // time), 4096 and 16 heads 140 against 112, of 64 columns 93 and 82, of 256 345 and
-// 217 (its registers spill around the exact pass).
+// 217. Full tiles of 64 columns spill 12 to 21 registers and 256 columns 29 to 44
+// (none in 16 bits) around the exact pass, which is inlined.
 // WINDOW: key numbers leave out what no row of the tile sees. Two prompts of up to
 // 6001 tokens and 16 heads of 64 columns through a window of 1024: 84 us, 458
 // TFLOP/s of what is seen, which is what this width reaches without a window.

@@ -356,8 +356,9 @@ class PagedCache:
         given. tree (int32 [tokens, words]): bit j of a row says whether it
         sees new token j of its sequence; without it a token sees the slots up
         to its own. window: of those only the last ``window``, and the first
-        ``sinks`` of the sequence (0: all); with a tree the new tokens that a
-        token sees come off its window first, and none of them is left out.
+        ``sinks`` of the sequence (0: all), which keep the positions they were
+        appended at; with a tree the new tokens that a token sees come off
+        its window first, and none of them is left out.
         max_ctx: the longest context to expect (shapes the launch
         only). workspace: a uint8 tensor of ``plan(...).workspace_bytes`` or
         more, not shared with calls that may run at the same time; made if
